@@ -9,4 +9,5 @@ from .sherry import (  # noqa: F401
     gemv_workspace_bytes, lib, library_path, pack, packed_bytes, workspace,
     GroupedGemvF32, quantize_f32, quantize_swiglu, gemv_f32, gemv_swiglu, gemv_f32_grouped,
     gemv_f32_workspace_bytes,
+    qk_norm_rope, kv4_cache, kv4_write, kv4_read, attn_kv4, attn_kv4_workspace_bytes,
 )

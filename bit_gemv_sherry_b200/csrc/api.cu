@@ -88,6 +88,7 @@ extern "C" const char *sherry_status_string(sherry_status s) {
         case SHERRY_ERR_CUDA: return "CUDA error (see sherry_last_error)";
         case SHERRY_ERR_TIMEOUT: return "a bounded device-side wait timed out";
         case SHERRY_ERR_WORKSPACE: return "workspace missing or too small";
+        case SHERRY_ERR_INDEX: return "a page table or a length names a page outside the cache";
     }
     return "unknown status";
 }

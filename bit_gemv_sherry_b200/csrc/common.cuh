@@ -46,6 +46,8 @@ struct OccupancyCache {
 
 // Reads and clears the error word of the GEMV kernels (after a device sync).
 sherry_status gemv_device_error();
+// The same for the kernels of the 4-bit cache and its attention.
+sherry_status kv4_device_error();
 
 // ---------------------------------------------------------------------------
 // Tile decode

@@ -500,8 +500,9 @@ extern "C" sherry_status sherry_device_error(void) {
             return SHERRY_ERR_CUDA;
         }
     }
-    // the GEMV kernels keep their own word; both are read and cleared
+    // the GEMV kernels and those of the 4-bit cache keep their own words; all are read and cleared
     const sherry_status g = sherry::gemv_device_error();
-    if (v == 0) return g;
+    const sherry_status a = sherry::kv4_device_error();
+    if (v == 0) return g != SHERRY_OK ? g : a;
     return static_cast<sherry_status>(v);
 }

@@ -18,7 +18,7 @@ _lib = None
 STATUS = {
     0: "SHERRY_OK", 1: "SHERRY_ERR_NULL", 2: "SHERRY_ERR_SHAPE", 3: "SHERRY_ERR_ALIGN",
     4: "SHERRY_ERR_UNSUPPORTED", 5: "SHERRY_ERR_CUDA", 6: "SHERRY_ERR_TIMEOUT",
-    7: "SHERRY_ERR_WORKSPACE",
+    7: "SHERRY_ERR_WORKSPACE", 8: "SHERRY_ERR_INDEX",
 }
 TILE_K = 128
 MAX_GEMV_BATCH = 16
@@ -49,6 +49,24 @@ class F32Desc(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("x", ctypes.c_void_p),
                 ("u", ctypes.c_void_p), ("y", ctypes.c_void_p), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("k_out", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("T", ctypes.c_int64),
+                ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int), ("R", ctypes.c_int),
+                ("in_type", ctypes.c_int), ("out_type", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
+class Kv4Args(ctypes.Structure):
+    _fields_ = [("cache", ctypes.c_void_p), ("pages", ctypes.c_int64), ("H", ctypes.c_int),
+                ("D", ctypes.c_int), ("page_table", ctypes.c_void_p), ("width", ctypes.c_int64),
+                ("table_stride", ctypes.c_int64), ("ctx_lens", ctypes.c_void_p),
+                ("cu_q", ctypes.c_void_p), ("B", ctypes.c_int64), ("T", ctypes.c_int64)]
 
 
 def library_path():
@@ -94,6 +112,12 @@ def lib():
         "sherry_cmp_transcode": ([i32, p, i64, i64, p, p], i32),
         "sherry_cmp_gemv_grouped": ([i32, p, i32, i32, p, sz, p], i32),
         "sherry_cmp_gemv_acc": ([i32, p, p, p, i64, i64, i32, p, sz, p], i32),
+        "sherry_qk_norm_rope": ([p, p], i32),
+        "sherry_kv4_bytes": ([i64, i32, i32], sz),
+        "sherry_kv4_write": ([p, p, p, i32, i64, i64, p], i32),
+        "sherry_kv4_read": ([p, p, p, i32, i64, i64, p], i32),
+        "sherry_attn_kv4_workspace_bytes": ([i64, i32, i32], sz),
+        "sherry_attn_kv4": ([p, p, i64, p, i64, i32, i64, ctypes.c_float, p, sz, p], i32),
         "sherry_probe_mma_i8": ([i32, p, p], i32),
         "sherry_device_error": ([], i32),
         "sherry_set_wait_limit": ([i64], i32),
@@ -625,6 +649,216 @@ class GroupedCmpGemv:
         s = ctypes.c_void_p(stream if stream is not None
                             else _stream_handle(self.device))
         _check(lib().sherry_cmp_gemv_grouped(*self.args, s), "sherry_cmp_gemv_grouped")
+
+
+# ----------------------------------------------------------------------------- attention
+KV4_PAGE = 64
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _heads(t, name, dev=None):
+    """(type, rows, heads, D, elements from row to row) of a [T, heads, D] tensor whose
+    rows are contiguous; the row stride is free (a slice of a fused product will do)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype not in _TYPES:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    if t.dim() != 3:
+        raise ValueError("%s must have shape [T, heads, D]" % name)
+    if dev is not None and t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError("%s must have contiguous rows (strides %s)" % (name, t.stride()))
+    return _TYPES[t.dtype], T, H, D, (st if T > 1 else H * D)
+
+
+def _index(t, name, dev, dim=1):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != dev:
+        raise TypeError("%s must be an int32 tensor on %s" % (name, dev))
+    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("%s must have %d dimension(s), the last contiguous" % (name, dim))
+
+
+def _vector(t, name, dev, n):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != dev:
+        raise TypeError("%s must be a float32 tensor on %s" % (name, dev))
+    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %d elements" % (name, n))
+
+
+def _call(dev, f, where, *args):
+    """f(*args, current stream of dev), with dev the current device."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream_handle(dev)), where)
+    else:
+        _check(f(*args, _stream_handle(dev)), where)
+
+
+def _scratch(nbytes, dev):
+    """As workspace(); a call under graph capture gets its own buffer from the graph's pool,
+    so that two graphs that run at the same time share none."""
+    with torch.cuda.device(dev):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return workspace(nbytes, dev)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-5,
+                 interleaved=False, q_out=None, k_out=None, out_dtype=None):
+    """Per-head RMS norm (where a weight [D] is given) and rotary positions of q [T, Hq, D] and
+    k [T, Hk, D] (fp32 or bf16; either may be None) in one launch.  positions int32 [T], inv_freq
+    fp32 [R / 2] (R <= D elements of a head turn).  Pairs are (j, j + R / 2), or (2 j, 2 j + 1) if
+    interleaved.  Returns (q_out, k_out) of out_dtype (default bfloat16); q_out may be q itself."""
+    if q is None and k is None:
+        raise TypeError("q or k must be given")
+    dev = (q if q is not None else k).device
+    a = RopeArgs()
+    shape = None
+    for t, out, w, side in ((q, q_out, q_weight, "q"), (k, k_out, k_weight, "k")):
+        if t is None:
+            if out is not None or w is not None:
+                raise TypeError("%s is None but %s_out or %s_weight is given" % (side, side, side))
+            continue
+        ty, T, H, D, stride = _heads(t, side, dev)
+        if out is None:
+            out = torch.empty((T, H, D), dtype=out_dtype or torch.bfloat16, device=dev)
+            if side == "q":
+                q_out = out
+            else:
+                k_out = out
+        oty, oT, oH, oD, ostride = _heads(out, side + "_out", dev)
+        if (oT, oH, oD) != (T, H, D):
+            raise ValueError("%s_out has shape %s, expected %s" % (side, (oT, oH, oD), (T, H, D)))
+        if shape not in (None, (ty, oty, T, D)):
+            raise ValueError("q and k differ in type, tokens or head size")
+        shape = (ty, oty, T, D)
+        if w is not None:
+            _vector(w, side + "_weight", dev, D)
+        wp = w.data_ptr() if w is not None else None
+        if side == "q":
+            a.q, a.q_out, a.q_stride, a.q_out_stride, a.q_weight, a.Hq = (
+                t.data_ptr(), out.data_ptr(), stride, ostride, wp, H)
+        else:
+            a.k, a.k_out, a.k_stride, a.k_out_stride, a.k_weight, a.Hk = (
+                t.data_ptr(), out.data_ptr(), stride, ostride, wp, H)
+    ty, oty, T, D = shape
+    _index(positions, "positions", dev)
+    if positions.numel() != T:
+        raise ValueError("positions has %d entries for %d tokens" % (positions.numel(), T))
+    _vector(inv_freq, "inv_freq", dev, inv_freq.numel())
+    a.positions, a.inv_freq = positions.data_ptr(), inv_freq.data_ptr()
+    a.T, a.D, a.R, a.in_type, a.out_type = T, D, 2 * inv_freq.numel(), ty, oty
+    a.interleaved, a.eps = int(interleaved), eps
+    _call(dev, lib().sherry_qk_norm_rope, "sherry_qk_norm_rope", ctypes.addressof(a))
+    return q_out, k_out
+
+
+def kv4_cache(pages, heads, dim, device):
+    """A zeroed 4-bit key/value cache, uint8 [pages, heads, 2, 64 * (dim / 2 + 4)]; dim 64 or 128."""
+    nbytes = int(lib().sherry_kv4_bytes(pages, heads, dim))
+    if nbytes == 0:
+        raise ValueError("no 4-bit cache of %d pages, %d heads of %d" % (pages, heads, dim))
+    return torch.zeros((pages, heads, 2, KV4_PAGE * (dim // 2 + 4)), dtype=torch.uint8, device=device)
+
+
+def _kv4(cache, page_table, ctx_lens, cu_q, T):
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dtype != torch.uint8:
+        raise TypeError("cache must be a uint8 CUDA tensor (kv4_cache)")
+    if cache.dim() != 4 or cache.shape[2] != 2 or not cache.is_contiguous():
+        raise ValueError("cache must be contiguous, [pages, heads, 2, 64 * (dim / 2 + 4)]")
+    dev = cache.device
+    pages, H, _, block = cache.shape
+    D = (block // KV4_PAGE - 4) * 2
+    if D not in (64, 128) or block != KV4_PAGE * (D // 2 + 4):
+        raise ValueError("cache blocks of %d bytes are of no head size" % block)
+    _index(page_table, "page_table", dev, 2)
+    _index(ctx_lens, "ctx_lens", dev)
+    B, width = page_table.shape
+    if ctx_lens.numel() != B:
+        raise ValueError("ctx_lens has %d entries, page_table %d rows" % (ctx_lens.numel(), B))
+    if cu_q is not None:
+        _index(cu_q, "cu_q", dev)
+        if cu_q.numel() != B + 1:
+            raise ValueError("cu_q has %d entries for %d sequences" % (cu_q.numel(), B))
+    elif T != B:
+        raise ValueError("%d rows for %d sequences: give cu_q" % (T, B))
+    return Kv4Args(cache.data_ptr(), pages, H, D, page_table.data_ptr(), width,
+                   page_table.stride(0) if B > 1 else width, ctx_lens.data_ptr(),
+                   cu_q.data_ptr() if cu_q is not None else None, B, T), dev
+
+
+def _kv4_pair(k, v, cache):
+    ty, T, H, D, ks = _heads(k, "k", cache.device)
+    vty, vT, vH, vD, vs = _heads(v, "v", cache.device)
+    if (ty, T, H, D) != (vty, vT, vH, vD):
+        raise ValueError("k and v differ in type or shape")
+    return ty, T, H, D, ks, vs
+
+
+def kv4_write(cache, k, v, page_table, ctx_lens, cu_q=None):
+    """Codes the new tokens' k and v [T, heads, dim] (fp32 or bf16) into the cache.  page_table int32
+    [B, width], ctx_lens int32 [B] (the new tokens included); rows cu_q[b] .. cu_q[b + 1] - 1 are the
+    last positions of sequence b (cu_q None: one row each)."""
+    ty, T, H, D, ks, vs = _kv4_pair(k, v, cache)
+    a, dev = _kv4(cache, page_table, ctx_lens, cu_q, T)
+    if (H, D) != (a.H, a.D):
+        raise ValueError("k has %d heads of %d, the cache %d of %d" % (H, D, a.H, a.D))
+    _call(dev, lib().sherry_kv4_write, "sherry_kv4_write", ctypes.addressof(a), k.data_ptr(), v.data_ptr(),
+          ty, ks, vs)
+
+
+def kv4_read(cache, page_table, ctx_lens, cu_q=None, rows=None, dtype=torch.float32, k=None, v=None):
+    """The values that the cache holds for the tokens that kv4_write takes: (k, v) [T, heads, dim].
+    Rows without a place in the cache are left as they are (zeros in tensors made here, of `rows`
+    rows; needed where cu_q is given)."""
+    if (k is None) != (v is None):
+        raise TypeError("give both k and v, or neither")
+    if k is None:
+        if rows is None:
+            if cu_q is not None:
+                raise TypeError("rows must be given with cu_q")
+            rows = ctx_lens.numel()
+        a, dev = _kv4(cache, page_table, ctx_lens, cu_q, rows)
+        k = torch.zeros((rows, a.H, a.D), dtype=dtype, device=dev)
+        v = torch.zeros((rows, a.H, a.D), dtype=dtype, device=dev)
+    ty, T, H, D, ks, vs = _kv4_pair(k, v, cache)
+    a, dev = _kv4(cache, page_table, ctx_lens, cu_q, T)
+    if (H, D) != (a.H, a.D):
+        raise ValueError("k has %d heads of %d, the cache %d of %d" % (H, D, a.H, a.D))
+    _call(dev, lib().sherry_kv4_read, "sherry_kv4_read", ctypes.addressof(a), k.data_ptr(), v.data_ptr(),
+          ty, ks, vs)
+    return k, v
+
+
+def attn_kv4_workspace_bytes(T, heads, dim):
+    return int(lib().sherry_attn_kv4_workspace_bytes(T, heads, dim))
+
+
+def attn_kv4(q, cache, page_table, ctx_lens, cu_q=None, max_q=0, scale=None, out=None, ws=None):
+    """Causal attention of the new tokens' q bf16 [T, Hq, dim] over the cache (their own keys and values
+    written before): out bf16 [T, Hq, dim].  page_table, ctx_lens and cu_q as for kv4_write; scale
+    defaults to dim ** -0.5; max_q, the most new tokens of a sequence, helps to pick kernels (0: not
+    known).  Rows without a position give zeros."""
+    ty, T, Hq, D, qs = _heads(q, "q", cache.device)
+    a, dev = _kv4(cache, page_table, ctx_lens, cu_q, T)
+    if out is None:
+        make = torch.empty if cu_q is None else torch.zeros  # rows outside every sequence stay
+        out = make((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    oty, oT, oH, oD, os_ = _heads(out, "out", dev)
+    if ty != 1 or oty != 1:
+        raise TypeError("q and out must be bfloat16")
+    if (oT, oH, oD) != (T, Hq, D):
+        raise ValueError("out has shape %s, expected %s" % ((oT, oH, oD), (T, Hq, D)))
+    if D != a.D or Hq % a.H:
+        raise ValueError("q has %d heads of %d, the cache %d of %d" % (Hq, D, a.H, a.D))
+    if ws is None:
+        ws = _scratch(attn_kv4_workspace_bytes(T, Hq, D), dev)
+    _call(dev, lib().sherry_attn_kv4, "sherry_attn_kv4", ctypes.addressof(a), q.data_ptr(), qs,
+          out.data_ptr(), os_, Hq, int(max_q), D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
+    return out
 
 
 def probe_mma_i8(iters, stream=None):

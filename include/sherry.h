@@ -81,7 +81,8 @@ typedef enum {
     SHERRY_ERR_UNSUPPORTED = 4, /* a size beyond what the kernels support (e.g. B > 16) */
     SHERRY_ERR_CUDA = 5,        /* a CUDA call or launch failed                         */
     SHERRY_ERR_TIMEOUT = 6,     /* a bounded device-side wait ran out (see below)       */
-    SHERRY_ERR_WORKSPACE = 7    /* workspace missing or smaller than required           */
+    SHERRY_ERR_WORKSPACE = 7,   /* workspace missing or smaller than required           */
+    SHERRY_ERR_INDEX = 8        /* a page table names no page of the cache (see below)  */
 } sherry_status;
 
 #define SHERRY_TILE_K 128         /* weights per tile                     */
@@ -448,11 +449,143 @@ sherry_status sherry_gemm_acc(const uint32_t *codes, const int8_t *x, int32_t *a
                               int64_t M, int64_t N, int64_t K, sherry_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Attention between the q, k, v products and the o product of a decoder layer:
+ * norm and rotation of queries and keys, a 4-bit key/value cache, attention
+ * over it.  The pages define none of it; LLaMA-3.2, the models the method is
+ * evaluated on (arXiv 2601.07892, abstract), needs all three around the GEMVs
+ * of its layers.
+ */
+
+/* Types of the ragged tensors below. */
+#define SHERRY_F32 0
+#define SHERRY_BF16 1
+
+/*
+ * sherry_qk_norm_rope -- RMS norm (where a weight is given) and rotary
+ * positions of queries and keys, both in one launch.  For a head x of D
+ * elements of the token at position pos:
+ *     n[i] = x[i] * (1 / sqrt(mean(x^2) + eps)) * w[i]   (w NULL: n = x),
+ *     a pair (a, b) of n turns by pos * inv_freq[j]:
+ *         (a cos - b sin, b cos + a sin),   j = 0 .. R / 2 - 1,
+ * the pair being (n[j], n[j + R / 2]), or (n[2 j], n[2 j + 1]) if `interleaved`;
+ * elements R .. D - 1 stay.  The angle is reduced in 64 bits, so that far
+ * positions keep theirs; everything else is fp32 and the result is rounded once.
+ *   q, k            [T][Hq][D], [T][Hk][D] of in_type, 16-byte aligned; *_stride
+ *                   elements from token to token, multiples of 4 (fp32) or 8 (bf16),
+ *                   at least heads * D.  A head count of 0 leaves that side out.
+ *   q_out, k_out    the same of out_type; an output may be its own input where
+ *                   type and stride agree, and overlaps no other tensor.
+ *   positions [T] int32, any sign.  inv_freq [R / 2] fp32.
+ *   q_weight, k_weight  [D] fp32, 16-byte aligned, or NULL.
+ *   D a multiple of 8 up to 256; R a multiple of 8, 0 <= R <= D (R = 0: norm only).
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED (a type, more than 2^31 - 1 rows), CUDA.
+ */
+typedef struct {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    const int32_t *positions;
+    const float *inv_freq;
+    const float *q_weight, *k_weight;
+    int64_t T;
+    int Hq, Hk, D, R;
+    int in_type, out_type;
+    int interleaved;
+    float eps;
+} sherry_rope;
+sherry_status sherry_qk_norm_rope(const sherry_rope *r, sherry_stream_t stream);
+
+/*
+ * The 4-bit cache: [pages][H][2] blocks (0: keys, 1: values) of
+ * SHERRY_KV4_PAGE = 64 tokens.  A block is 64 rows of D / 2 code bytes (element
+ * 2 i in the low four bits of byte i, 2 i + 1 in the high ones) and then 64
+ * pairs of bf16 (step s, low end m); an element stands for m + s * code.  A row x
+ * is coded by
+ *     s = bf16((max - min) * fl32(1 / 15)),  m = bf16(min),
+ *     code = clamp(rint((x - m) * (1 / s)), 0, 15),
+ * every operation in fp32 with round-to-nearest-even; s below 2^-120 gives s = 0
+ * and codes 0; a row whose max - min, s or m is not finite (NaN, Inf, or a spread
+ * beyond fp32) gets s = m = NaN and codes 0 and reads back as NaN.
+ *
+ * A sherry_kv4 names a cache and a batch of B sequences in it:
+ *   cache       sherry_kv4_bytes(pages, H, D) bytes, 16-byte aligned.
+ *   page_table  [B][table_stride] int32, the first `width` of a row used: position p
+ *               of sequence b is in slot p % 64 of page page_table[b][p / 64].
+ *               Entries past a sequence's length are not read.
+ *   ctx_lens    [B] int32, tokens of each sequence, the new ones included.
+ *   cu_q        [B + 1] int32, ascending: rows cu_q[b] .. cu_q[b + 1] - 1 of the ragged
+ *               tensors are the last positions of sequence b.  NULL: B = T, one each.
+ *   T           rows of the ragged tensors.  Rows outside every sequence are left as they are.
+ * A sequence shorter than its rows (an empty slot of a padded batch) has no place
+ * for the first of them: the write and the read pass them over, the attention gives zeros.
+ * These four are device arrays read by the kernels; nothing is read outside the tensors
+ * whatever they hold.  A page number outside 0 .. pages - 1, or a length beyond the table,
+ * records SHERRY_ERR_INDEX for sherry_device_error(): the write and the read pass such
+ * tokens over, the attention treats them as not there.
+ * Two rows of one call that share a slot (sequences with a common page, written) race:
+ * the slot then holds either row or a mixture.
+ */
+#define SHERRY_KV4_PAGE 64
+typedef struct {
+    void *cache;
+    int64_t pages;
+    int H, D;                /* key/value heads; elements per head, 64 or 128 */
+    const int32_t *page_table;
+    int64_t width, table_stride;
+    const int32_t *ctx_lens;
+    const int32_t *cu_q;
+    int64_t B, T;
+} sherry_kv4;
+
+/* Bytes of a cache (0 for a shape that the calls do not take). */
+size_t sherry_kv4_bytes(int64_t pages, int H, int D);
+
+/*
+ * sherry_kv4_write -- codes the new tokens' keys and values into the cache.
+ * sherry_kv4_read  -- the values that the cache holds for the same tokens.
+ *   k, v  [T][H][D] of `type`, 16-byte aligned; strides in elements from token to
+ *         token, multiples of 4 (fp32) or 8 (bf16), at least H * D.
+ * The values are exact in fp32 (m + s * code rounded once), rounded once more to bf16.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED (D, a type), CUDA; INDEX through
+ * sherry_device_error.
+ */
+sherry_status sherry_kv4_write(const sherry_kv4 *c, const void *k, const void *v, int type,
+                               int64_t k_stride, int64_t v_stride, sherry_stream_t stream);
+sherry_status sherry_kv4_read(const sherry_kv4 *c, void *k, void *v, int type, int64_t k_stride,
+                              int64_t v_stride, sherry_stream_t stream);
+
+/*
+ * sherry_attn_kv4 -- causal attention of the new tokens over the cache (their own
+ * keys and values included: write them first).  For the row at position pos and
+ * head h, with the cache's head h / (Hq / H):
+ *     out = sum_t p[t] v[t],  p = softmax over t = 0 .. pos of scale * (q . k[t]),
+ * with k and v the values the cache holds.  A row without a position (pos < 0) gives zeros.
+ * Products are taken on the codes, which bf16 holds exactly; sums and softmax statistics
+ * are fp32; a probability times its token's step is rounded to bf16 for the second product,
+ * and the result once to bf16.
+ *   q    [T][Hq][D] bf16, 16-byte aligned, q_stride as above; Hq a multiple of H.
+ *   out  [T][Hq][D] bf16, likewise.
+ *   max_q      the most new tokens a sequence has, as far as the caller knows (0: not known).
+ *              It picks kernels and changes no result beyond rounding.
+ *   workspace  sherry_attn_kv4_workspace_bytes(T, Hq, D) bytes, 256-byte aligned; its
+ *              contents are scratch.  Calls that overlap on the GPU must not share it.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED (D), WORKSPACE, CUDA; INDEX and TIMEOUT through
+ * sherry_device_error.
+ */
+size_t sherry_attn_kv4_workspace_bytes(int64_t T, int Hq, int D);
+sherry_status sherry_attn_kv4(const sherry_kv4 *c, const uint16_t *q, int64_t q_stride,
+                              uint16_t *out, int64_t out_stride, int Hq, int64_t max_q,
+                              float scale, void *workspace, size_t workspace_bytes,
+                              sherry_stream_t stream);
+
+/*
  * Device-side error word.  Kernels that wait on barriers bound every wait;
  * when one runs out the kernel records SHERRY_ERR_TIMEOUT here, releases what
- * it holds and returns instead of hanging.  sherry_device_error() synchronises
- * the current device, returns the recorded status (SHERRY_OK if none) and
- * clears it.
+ * it holds and returns instead of hanging.  The cache and attention calls record
+ * SHERRY_ERR_INDEX for page numbers outside the cache.  sherry_device_error()
+ * synchronises the current device, returns the recorded status (SHERRY_OK if
+ * none) and clears it.
  */
 sherry_status sherry_device_error(void);
 

@@ -1,0 +1,491 @@
+"""GPU parity of the attention-side operators against the 64-bit oracle (oracle/attn.py):
+norm and rotation, the 4-bit cache, attention over it, and the three between two GEMVs.
+
+Tolerances, from the arithmetic (u = 2^-24, a rounding to bf16 at most 2^-8 relative):
+
+rotation  cos and sin: the fraction of a turn is rounded once (2^-26 turns = 2 pi 2^-26 rad <
+          2^-23.3) and sincospi is within 2 ulp (2^-23): below 2^-22 in all.  The two products
+          and the sum round three times, (|a| + |b|) 3 u.  Together (|a| + |b|) 2^-21.3; taken
+          as 2^-21.  With a norm the sum of squares (at most 8 additions deep: 2 per lane, 5
+          shuffles, and a rounding per square), the mean, the sum with eps, the root, the
+          quotient and two products add at most 16 u relative: 2^-20, in all (|a| + |b|) 2^-19.
+cache     codes, steps and low ends are equal bit for bit (one rounding after another, in the
+          same order); read back, fl32(m + s c) is exact and bf16 rounds that once more.
+attention x_t = scale * q.k_t is summed in fp32 on codes held as 128 + c <= 143: D / 8 sums of
+          16 products, each sum and the two operations after it rounded by at most 2^-23 of the
+          largest partial result, so |dx| <= |scale| * sum|q| * 143 * max s * (D / 8 + 4) * 2^-23
+          plus the low end's share, |m~ - 136 s| <= |m| + 136 s, three roundings.  A probability is off by |dx| and by the exponential's
+          2^-21, so the output by 2 |dx| + 2^-20 times max |v|.  Rounding p s to bf16 moves the
+          output by 2^-8 sum p s |c - 8| <= 2^-8 * 8 * max s_v; the last rounding by 2^-8 |o|;
+          fp32 sums over L tokens by sqrt-free L 2^-23 of max|v| (L <= 2000: 2^-12).
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from bit_gemv_sherry_b200 import sherry as S
+from oracle import attn as A
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def np_of(t):
+    return t.float().cpu().numpy()
+
+
+def bf16_randn(rng, shape, mag=1.0):
+    return A.to_bf16((rng.standard_normal(shape) * mag).astype(np.float32))
+
+
+# ----------------------------------------------------------------------------- rotation
+def run_rope(T, hq, hk, D, R, src, dst, norm, inter, seed, far=131071, pad=0):
+    rng = np.random.default_rng(seed)
+    f = (500000.0 ** (-np.arange(0, R, 2) / max(R, 1))).astype(np.float32)
+    pos = rng.integers(-far if seed % 2 else 0, far + 1, T).astype(np.int32)
+    pos[0] = far
+    xs, ws, ins, outs = [], [], [], []
+    for h in (hq, hk):
+        x = bf16_randn(rng, (T, h, D), 3.0) if src == BF else (rng.standard_normal((T, h, D)) * 3).astype(np.float32)
+        w = (1 + 0.3 * rng.standard_normal(D)).astype(np.float32) if norm else None
+        big = torch.full((T, h * D + pad), float("nan"), dtype=src, device="cuda")
+        big[:, :h * D] = torch.from_numpy(x).reshape(T, h * D).to(src)
+        obig = torch.full((T, h * D + pad), 77.0, dtype=dst, device="cuda")
+        xs.append(x), ws.append(w)
+        ins.append(big[:, :h * D].unflatten(1, (h, D))), outs.append((obig, obig[:, :h * D].unflatten(1, (h, D))))
+    dw = [None if w is None else torch.from_numpy(w).cuda() for w in ws]
+    q, k = S.qk_norm_rope(ins[0], ins[1], torch.from_numpy(pos).cuda(), torch.from_numpy(f).cuda(), q_weight=dw[0],
+                          k_weight=dw[1], eps=1e-5, interleaved=inter, q_out=outs[0][1], k_out=outs[1][1])
+    for x, w, o, (obig, _), h in zip(xs, ws, (q, k), outs, (hq, hk)):
+        ref = A.rope(x, w, pos, f, 1e-5, inter)
+        y = x.astype(np.float64) if w is None else A.rope(x, w, pos, f[:0], 1e-5, inter)
+        mag = np.abs(y)
+        half = R // 2
+        ia = slice(0, R, 2) if inter else slice(0, half)
+        ib = slice(1, R, 2) if inter else slice(half, R)
+        tol = mag.copy()
+        tol[..., ia] = tol[..., ib] = mag[..., ia] + mag[..., ib]
+        tol = tol * (2.0 ** -19 if norm else 2.0 ** -21)
+        if dst == BF:
+            tol = tol + np.abs(ref) * 2.0 ** -8
+        err = np.abs(np_of(o).astype(np.float64) - ref)
+        assert np.all(err <= tol), (err - tol).max()
+        assert pad == 0 or torch.all(obig[:, h * D:] == 77.0)
+    assert S.device_error() == 0
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("src,dst", [(torch.float32, BF), (BF, BF), (torch.float32, torch.float32), (BF, torch.float32)])
+@pytest.mark.parametrize("T,hq,hk,D,R,norm", [
+    (1, 32, 8, 64, 64, False), (5, 3, 1, 128, 128, True), (130, 8, 2, 128, 64, True), (7, 5, 5, 64, 32, True),
+])
+def test_rope_matches_oracle(T, hq, hk, D, R, norm, src, dst, inter):
+    run_rope(T, hq, hk, D, R, src, dst, norm, inter, seed=T + R)
+
+
+@pytest.mark.parametrize("D,R", [(8, 8), (16, 8), (24, 24), (32, 16), (40, 40), (72, 72), (80, 40), (96, 96), (112, 8),
+                                 (136, 136), (192, 128), (256, 256), (256, 64), (64, 0), (200, 144)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_odd_head_sizes_and_strides(D, R, inter):
+    run_rope(9, 7, 2, D, R, torch.float32, BF, D % 16 == 0, inter, seed=D, pad=16)
+
+
+def test_rope_one_side_and_in_place():
+    x = torch.randn(4, 6, 64, device="cuda")
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    f = torch.rand(32, device="cuda")
+    q, k = S.qk_norm_rope(x, None, pos, f, out_dtype=torch.float32)
+    _, k2 = S.qk_norm_rope(None, x, pos, f, out_dtype=torch.float32)
+    assert k is None and torch.equal(q, k2)
+    y = x.clone()
+    S.qk_norm_rope(y, None, pos, f, q_out=y)
+    assert torch.equal(y, q)
+
+
+def test_rope_zero_rows_and_nan_stay_in_their_row():
+    x = torch.randn(3, 4, 64, device="cuda")
+    x[1, 2] = 0
+    x[0, 1, 5] = float("nan")
+    w = torch.ones(64, device="cuda")
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    q, _ = S.qk_norm_rope(x, None, pos, torch.rand(32, device="cuda"), q_weight=w, eps=1e-5)
+    assert not q[1, 2].any()
+    bad = torch.isnan(q).any(-1)
+    assert bad[0, 1] and bad.sum() == 1
+
+
+# ----------------------------------------------------------------------------- batches
+class Batch:
+    """Sequences in shuffled pages; unused slots, pages and table entries hold poison."""
+
+    def __init__(self, ctx, new, H, D, seed, extra_rows=0, spare=2):
+        rng = self.rng = np.random.default_rng(seed)
+        self.ctx, self.new, self.H, self.D = ctx, new, H, D
+        need = [(c + 63) // 64 for c in ctx]
+        self.width = max(max(need), 1) + 1
+        self.pages = sum(need) + spare
+        order = rng.permutation(self.pages)
+        self.table = np.full((len(ctx), self.width), -7, np.int32)
+        self.table[:, 1::2] = 1 << 30
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        self.T = int(self.cu[-1]) + extra_rows
+        self.one = all(n == 1 for n in new) and extra_rows == 0
+        self.cache = np.full((self.pages, H, 2, 64 * (D // 2 + 4)), 0xFF, np.uint8)   # codes 15, NaN pairs
+
+    def fill(self, kmag=1.0, vmag=1.0):
+        """Keys and values of every position; returns the values that the cache holds."""
+        self.kv = []
+        for b, c in enumerate(self.ctx):
+            vals = []
+            for kv in range(2):
+                x = (self.rng.standard_normal((self.H, c, self.D)) * (vmag if kv else kmag)).astype(np.float32)
+                if not kv:
+                    x += (self.rng.standard_normal((self.H, 1, self.D)) * kmag).astype(np.float32)
+                codes, s, m = A.kv4_encode(x)
+                for h in range(self.H):
+                    for t in range(c):
+                        A.kv4_pack(self.cache, self.table[b, t // 64], t % 64, h, kv, codes[h, t], s[h, t], m[h, t])
+                vals.append((A.kv4_values(codes, s, m), s, m))
+            self.kv.append(vals)
+        return self
+
+    def dev(self):
+        self.d_cache = torch.from_numpy(self.cache).cuda()
+        self.d_table = torch.from_numpy(self.table).cuda()
+        self.d_lens = torch.tensor(self.ctx, dtype=torch.int32, device="cuda")
+        self.d_cu = None if self.one else torch.from_numpy(self.cu).cuda()
+        return self
+
+
+RAGGED = [
+    ([1], [1]), ([64], [1]), ([65], [1]), ([130], [130]), ([200, 1, 0, 63, 128], [1] * 5),
+    ([70, 5, 0, 64, 300], [9, 5, 2, 1, 17]), ([3, 2], [7, 2]),   # more rows than tokens: no place for the first
+]
+
+
+# ----------------------------------------------------------------------------- cache
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("D,H", [(64, 3), (128, 2)])
+@pytest.mark.parametrize("ctx,new", RAGGED)
+def test_cache_write_and_read(ctx, new, D, H, dtype):
+    bt = Batch(ctx, new, H, D, seed=len(ctx) + D, extra_rows=0 if all(n == 1 for n in new) else 3).dev()
+    rng = bt.rng
+    mags = np.array([1.0, 1e-3, 300.0, 1e-30, 1e30], np.float32)[rng.integers(0, 5, bt.T)][:, None, None]
+    x = [A.to_bf16(v) if dtype == BF else v for v in
+         [(rng.standard_normal((bt.T, H, D)) * mags).astype(np.float32) for _ in range(2)]]
+    x[0][0, 0, 3] = np.nan
+    x[1][0, 0, :] = 2.5
+    pad = 8
+    big = [torch.zeros((bt.T, H * D + pad), dtype=dtype, device="cuda") for _ in range(2)]
+    view = [t[:, :H * D].unflatten(1, (H, D)) for t in big]
+    for v, a in zip(view, x):
+        v.copy_(torch.from_numpy(a))
+    S.kv4_write(bt.d_cache, view[0], view[1], bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+    expect, back = bt.cache.copy(), [np.full((bt.T, H, D), 77.0, np.float32) for _ in range(2)]
+    for kv in range(2):
+        codes, s, m = A.kv4_encode(x[kv])
+        vals = A.kv4_values(codes, s, m).astype(np.float32)
+        for b, (c, n) in enumerate(zip(ctx, new)):
+            for i in range(n):
+                p, t = c - n + i, bt.cu[b] + i
+                if p < 0:
+                    continue
+                for h in range(H):
+                    A.kv4_pack(expect, bt.table[b, p // 64], p % 64, h, kv, codes[t, h], s[t, h], m[t, h])
+                back[kv][t] = A.to_bf16(vals[t]) if dtype == BF else vals[t]
+    got = bt.d_cache.cpu().numpy()
+    nan_pair = np.array([0x7FFF, 0x7FFF], np.uint16).view(np.uint8)
+    for kv in range(2):   # a NaN's bits are the library's own
+        nan = A.kv4_encode(x[kv])[1]
+        for b, (c, n) in enumerate(zip(ctx, new)):
+            for i in range(n):
+                p = c - n + i
+                for h in range(H):
+                    if p >= 0 and np.isnan(nan[bt.cu[b] + i, h]):
+                        at = 32 * D + 4 * (p % 64)
+                        expect[bt.table[b, p // 64], h, kv, at:at + 4] = nan_pair
+    assert np.array_equal(got, expect)
+    out = [torch.full((bt.T, H * D + pad), 77.0, dtype=dtype, device="cuda") for _ in range(2)]
+    k, v = S.kv4_read(bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu,
+                      k=out[0][:, :H * D].unflatten(1, (H, D)), v=out[1][:, :H * D].unflatten(1, (H, D)))
+    assert np.array_equal(np_of(k), back[0], equal_nan=True)
+    assert np.array_equal(np_of(v), back[1], equal_nan=True)
+    assert torch.all(out[0][:, H * D:] == 77.0)
+    assert S.device_error() == 0
+
+
+def test_read_makes_its_own_tensors():
+    bt = Batch([5, 64], [1, 1], 2, 64, seed=4).fill().dev()
+    k, v = S.kv4_read(bt.d_cache, bt.d_table, bt.d_lens)
+    for b, c in enumerate(bt.ctx):
+        assert np.array_equal(np_of(k)[b], bt.kv[b][0][0][:, c - 1].astype(np.float32))
+        assert np.array_equal(np_of(v)[b], bt.kv[b][1][0][:, c - 1].astype(np.float32))
+
+
+# ----------------------------------------------------------------------------- attention
+def attn_bound(q, kv, ref, scale):
+    """Per row [n, D]: the bound of the module's head."""
+    (k, ks, km), (v, vs, vm) = kv
+    D = q.shape[-1]
+    sq = np.abs(q).sum(-1, keepdims=True)
+    smax, mmax = np.max(ks, initial=0.0), np.max(np.abs(km), initial=0.0)
+    dx = abs(scale) * sq * 2.0 ** -23 * (143.0 * smax * (D // 8 + 4) + 3 * (mmax + 136.0 * smax))
+    vmax = np.max(np.abs(v), initial=0.0)
+    return (2 * dx + 2.0 ** -12) * vmax + 2.0 ** -8 * 8 * np.max(vs, initial=0.0) + 2.0 ** -8 * np.abs(ref)
+
+
+def check_attn(bt, q, out, hq, scale, sentinel=None):
+    g = hq // bt.H
+    o = np_of(out).astype(np.float64)
+    for b, (c, n) in enumerate(zip(bt.ctx, bt.new)):
+        r = slice(bt.cu[b], bt.cu[b] + n)
+        last = c - n + np.arange(n)
+        for j in range(hq):
+            h = j // g
+            kv = [(x[h], s[h], m[h]) for x, s, m in bt.kv[b]]
+            ref = A.attend(q[r, j].astype(np.float64), kv[0][0], kv[1][0], last, scale)
+            tol = attn_bound(q[r, j], kv, ref, scale)
+            err = np.abs(o[r, j] - ref)
+            assert np.all(err <= tol), (b, j, np.nanmax(err - tol), np.isnan(err).sum())
+            assert not o[r, j][last < 0].any()
+    if sentinel is not None:
+        assert np.all(o[bt.cu[-1]:] == sentinel)
+
+
+def run_attn(ctx, new, hq, H, D, seed, qmag=1.0, scale=None, extra=0, max_q=0, pad=0):
+    bt = Batch(ctx, new, H, D, seed, extra_rows=extra).fill().dev()
+    q = bf16_randn(bt.rng, (bt.T, hq, D), qmag)
+    big = torch.full((bt.T, hq * D + pad), float("nan"), dtype=BF, device="cuda")
+    big[:, :hq * D] = torch.from_numpy(q).reshape(bt.T, hq * D)
+    obig = torch.full((bt.T, hq * D + pad), 77.0, dtype=BF, device="cuda")
+    out = S.attn_kv4(big[:, :hq * D].unflatten(1, (hq, D)), bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu,
+                     max_q=max_q, scale=scale, out=obig[:, :hq * D].unflatten(1, (hq, D)))
+    assert S.device_error() == 0
+    check_attn(bt, q, out, hq, D ** -0.5 if scale is None else scale, 77.0 if extra else None)
+    assert pad == 0 or torch.all(obig[:, hq * D:] == 77.0)
+    return bt, q, out
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,H", [(4, 1), (8, 8), (6, 2), (16, 1), (20, 1)])
+@pytest.mark.parametrize("ctx,new", RAGGED)
+def test_attn_matches_oracle(ctx, new, hq, H, D):
+    run_attn(ctx, new, hq, H, D, seed=sum(ctx) + hq, extra=0 if all(n == 1 for n in new) else 3,
+             max_q=max(new) if sum(ctx) % 2 else 0, pad=8)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,new,hq,H", [
+    ([1500], [1], 4, 1),                       # one long sequence: split over the machine
+    ([900, 17, 1300, 0, 64], [1] * 5, 8, 2),
+    ([300], [300], 8, 2),                      # a prompt: several tiles of rows
+    ([700, 40, 513], [200, 40, 129], 4, 2),    # prompts behind a context, one without
+    ([700, 800, 0, 90], [150, 1, 1, 2], 6, 2),  # a prompt and single tokens in one batch
+    ([257], [256], 1, 1), ([640], [33], 3, 1),
+])
+def test_attn_longer(ctx, new, hq, H, D):
+    for max_q in (0, max(new)):
+        run_attn(ctx, new, hq, H, D, seed=len(ctx) * 7 + hq + D, max_q=max_q,
+                 extra=0 if all(n == 1 for n in new) else 2)
+
+
+@pytest.mark.parametrize("new", [[1], [140]])
+def test_attn_peaked_scores_and_large_values(new):
+    run_attn([333], new, 4, 2, 64, seed=5, qmag=30.0)
+    run_attn([333], new, 4, 2, 128, seed=6, qmag=1e-4)
+    run_attn([333], new, 4, 2, 64, seed=7, scale=0.0)
+    run_attn([333], new, 4, 2, 64, seed=8, scale=-0.3)
+
+
+@pytest.mark.parametrize("new", [1, 200])
+def test_attn_max_q_too_small_changes_nothing_but_rounding(new):
+    run_attn([260, 230], [new, new], 4, 2, 64, seed=9, max_q=1)
+
+
+@pytest.mark.parametrize("new", [1, 150])
+def test_attn_is_deterministic_and_graph_safe(new):
+    bt, q, out = run_attn([800, 650, 150], [new] * 3, 8, 2, 64, seed=11)
+    dq = torch.from_numpy(q).cuda().bfloat16()
+    ref = S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+    again = S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+    assert torch.equal(ref, again) and torch.equal(ref, out)
+    # two graphs replayed at the same time share no scratch
+    outs, graphs = [], []
+    for _ in range(2):
+        o = torch.empty_like(ref)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu, out=o)
+        outs.append(o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+    # lengths that change between replays are read anew
+    bt.d_lens.copy_(torch.tensor([800, 64, 1], dtype=torch.int32))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu))
+    assert S.device_error() == 0
+
+
+def test_attn_two_streams_at_once():
+    bt, q, out = run_attn([800, 650, 150], [1] * 3, 8, 2, 128, seed=12)
+    dq = torch.from_numpy(q).cuda().bfloat16()
+    torch.cuda.synchronize()
+    res = []
+    for _ in range(6):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            res.append([S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens) for _ in range(4)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(r, out) for rs in res for r in rs)
+
+
+# ----------------------------------------------------------------------------- bad indexes
+@pytest.mark.parametrize("new", [1, 100])
+@pytest.mark.parametrize("bad", [-1, 1 << 20, "width"])
+def test_bad_pages_are_recorded_and_passed_over(bad, new):
+    ctx = [300, 200]
+    bt = Batch(ctx, [new] * 2, 2, 64, seed=13).fill()
+    if bad == "width":   # a length beyond the table: the tokens past it are not there
+        bt.dev()
+        cut = 64 * 3
+        bt.d_table = bt.d_table[:, :3].contiguous()
+    else:
+        cut = None
+        hole = 1         # tokens 64 .. 127 of sequence 0
+        bt.table[0, hole] = bad
+        bt.dev()
+    q = bf16_randn(bt.rng, (2 * new, 4, 64))
+    out = S.attn_kv4(torch.from_numpy(q).cuda().bfloat16(), bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+    assert S.device_error() == 8 and S.device_error() == 0
+    o = np_of(out)
+    for b, c in enumerate(ctx):
+        there = np.ones(c, bool)
+        if cut is not None:
+            there[cut:] = False
+        elif b == 0:
+            there[64:128] = False
+        for j in range(4):
+            kv = [(x[j // 2][there], s[j // 2][there], m[j // 2][there]) for x, s, m in bt.kv[b]]
+            last = np.array([there[:c - new + i + 1].sum() - 1 for i in range(new)])
+            r = slice(b * new, (b + 1) * new)
+            ref = A.attend(q[r, j].astype(np.float64), kv[0][0], kv[1][0], last, 0.125)
+            assert np.all(np.abs(o[r, j] - ref) <= attn_bound(q[r, j], kv, ref, 0.125))
+    # the write and the read pass such tokens over
+    x = torch.randn(2 * new, 2, 64, device="cuda")
+    before = bt.d_cache.clone()
+    t2 = torch.full_like(bt.d_table, bt.pages if bad == "width" else bad)
+    S.kv4_write(bt.d_cache, x, x, t2, bt.d_lens, cu_q=bt.d_cu)
+    assert S.device_error() == 8
+    assert torch.equal(before, bt.d_cache)
+    k, v = S.kv4_read(bt.d_cache, t2, bt.d_lens, cu_q=bt.d_cu, rows=2 * new)
+    assert S.device_error() == 8 and not k.any() and not v.any()
+
+
+@pytest.mark.parametrize("cu", [[0, -5, 40], [40, 10, 0], [0, 1 << 30, 40], [-9, 20, 1 << 30], [7, 7, 7]])
+def test_malformed_row_offsets_stay_in_bounds(cu):
+    bt = Batch([100, 90], [20, 20], 2, 64, seed=14).fill().dev()
+    d_cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    q = torch.randn(40, 4, 64, device="cuda").bfloat16()
+    guard = torch.full((42, 4, 64), 77.0, dtype=BF, device="cuda")
+    for max_q in (0, 1):
+        S.attn_kv4(q, bt.d_cache, bt.d_table, bt.d_lens, cu_q=d_cu, max_q=max_q, out=guard[1:41])
+    x = torch.randn(40, 2, 64, device="cuda")
+    S.kv4_write(bt.d_cache, x, x, bt.d_table, bt.d_lens, cu_q=d_cu)
+    S.kv4_read(bt.d_cache, bt.d_table, bt.d_lens, cu_q=d_cu, rows=40)
+    S.device_error()
+    assert torch.all(guard[0] == 77.0) and torch.all(guard[41] == 77.0)
+
+
+def test_negative_lengths_are_empty():
+    bt = Batch([100, 90], [1, 1], 2, 64, seed=15).fill().dev()
+    lens = torch.tensor([-3, 90], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    out = S.attn_kv4(q, bt.d_cache, bt.d_table, lens)
+    assert not out[0].any() and out[1].any() and S.device_error() == 0
+
+
+def test_nan_in_a_visible_token_reaches_only_its_rows():
+    bt = Batch([70, 80], [1, 1], 2, 64, seed=16).fill()
+    at = 64 * 32 + 4 * 5
+    bt.cache[bt.table[0, 0], 1, 0, at:at + 4] = 0xFF    # key 5 of sequence 0, head 1
+    bt.dev()
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    out = S.attn_kv4(q, bt.d_cache, bt.d_table, bt.d_lens)
+    bad = torch.isnan(out).any(-1)
+    assert bad[0, 2:].all() and not bad[0, :2].any() and not bad[1].any()
+
+
+# ----------------------------------------------------------------------------- together
+@pytest.mark.parametrize("D,hq,H", [(64, 8, 2), (128, 4, 2)])
+def test_attention_block_between_gemvs(D, hq, H):
+    """Three decode steps of two sequences: q, k, v GEMVs -> rotation -> cache write -> attention ->
+    o GEMV, against the same steps through the oracle from each stage's own device inputs."""
+    dim, B = 512, 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+
+    def w(n, k):
+        return S.pack(torch.randn(n, k, generator=g, device="cuda") * 0.05)
+
+    (wq, sq), (wk, sk), (wv, sv), (wo, so) = w(hq * D, dim), w(H * D, dim), w(H * D, dim), w(dim, hq * D)
+    f = (500000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().cuda()
+    cache = S.kv4_cache(5, H, D, "cuda")
+    table = torch.tensor([[3, 1], [0, 4]], dtype=torch.int32, device="cuda")
+    held = [[], []]
+    for step in range(3):
+        lens = torch.tensor([step + 1, step + 1], dtype=torch.int32, device="cuda")
+        pos = lens - 1
+        x = torch.randn(B, dim, generator=g, device="cuda").bfloat16()
+        q = torch.empty(B, hq * D, device="cuda")
+        k, v = torch.empty(B, H * D, device="cuda"), torch.empty(B, H * D, device="cuda")
+        S.gemv_bf16_grouped([(wq, sq, x, q), (wk, sk, x, k), (wv, sv, x, v)], B=B)
+        qr, kr = S.qk_norm_rope(q.view(B, hq, D), k.view(B, H, D), pos, f, out_dtype=BF)
+        S.kv4_write(cache, kr, v.view(B, H, D).bfloat16(), table, lens)
+        o = S.attn_kv4(qr, cache, table, lens)
+        y = S.gemv_bf16(wo, so, o.view(B, hq * D))
+        ref = A.rope(np_of(k).reshape(B, H, D), None, pos.cpu().numpy(), f.cpu().numpy(), 0.0, False)
+        assert np.all(np.abs(np_of(kr) - ref) <= np.abs(ref) * 2.0 ** -8 + np.abs(np_of(k)).max() * 2.0 ** -20)
+        kk, ks, km = A.kv4_encode(np_of(kr))
+        vv, vs, vm = A.kv4_encode(np_of(v.bfloat16()).reshape(B, H, D))
+        for b in range(B):
+            held[b].append((A.kv4_values(kk, ks, km)[b], ks[b], km[b], A.kv4_values(vv, vs, vm)[b], vs[b], vm[b]))
+            for j in range(hq):
+                h = j // (hq // H)
+                kv = [tuple(np.stack([t[3 * i + e][h] for t in held[b]]) for e in range(3)) for i in range(2)]
+                qj = np_of(qr)[b, j][None]
+                r = A.attend(qj.astype(np.float64), kv[0][0], kv[1][0], [step], D ** -0.5)
+                assert np.all(np.abs(np_of(o)[b, j] - r[0]) <= attn_bound(qj, kv, r, D ** -0.5)[0])
+        assert torch.equal(y, S.gemv_bf16(wo, so, o.view(B, hq * D).clone())) and torch.isfinite(y).all()
+    assert S.device_error() == 0
+
+
+def test_c_entry_with_a_strided_table_and_workspace_of_the_stated_size():
+    bt, q, out = run_attn([90, 300], [1, 1], 4, 2, 64, seed=21)
+    wide = torch.full((2, bt.width + 3), -1, dtype=torch.int32, device="cuda")
+    wide[:, :bt.width] = bt.d_table
+    dq = torch.from_numpy(q).cuda().bfloat16()
+    o = torch.empty_like(out)
+    need = S.attn_kv4_workspace_bytes(2, 4, 64)
+    ws = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    a = S.Kv4Args(bt.d_cache.data_ptr(), bt.pages, 2, 64, wide.data_ptr(), bt.width, wide.stride(0),
+                  bt.d_lens.data_ptr(), None, 2, 2)
+    st = S.lib().sherry_attn_kv4(ctypes.addressof(a), dq.data_ptr(), 256, o.data_ptr(), 256, 4, 1, 0.125,
+                                 ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and torch.all(ws[need:] == 0xA5)
+    assert torch.equal(S.attn_kv4(dq, bt.d_cache, wide[:, :bt.width], bt.d_lens), out)

@@ -13,7 +13,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsherry.so")
-SOURCES = ["api.cu", "pack.cu", "gemv.cu", "gemm.cu", "rope.cu", "kv4.cu", "attn.cu"]
+SOURCES = ["api.cu", "pack.cu", "gemv.cu", "gemm.cu", "rope.cu", "kv4.cu", "attn.cu",
+           "attn_tile.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -1,25 +1,11 @@
 // attn.cu -- causal attention over the 4-bit key/value cache: the calls, and the kernels for
 // sequences with few new tokens (decode steps, drafts).
-//
-// For a row q (a new token and a query head) and the tokens t it sees,
-//     out = sum_t p_t v_t / sum_t p_t,   p_t = 2^(x_t - m),   x_t = scale log2(e) (q . k_t).
-// With k_t = m_t + s_t c_t and c_t in 0 .. 15,  q . k_t = s_t (q . c_t) + m_t sum(q): the first
-// product runs on the codes, which bf16 holds exactly, and the step and low end come in after it.
-// Likewise sum_t p_t v_t = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (m_t + 8 s_t), where p_t s_t is
-// rounded to bf16 for the second product (its error is that of a bf16 probability) and the rest
-// stays in fp32.  A code becomes a bf16 by one AND-OR: 0x4300 | c is 128 + c.  The 128 is taken
-// out of the first product by starting it at -128 sum(q) and out of the second by -136 times the
-// sum of the rounded p s.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 
-#include "kv4.cuh"
+#include "attn.cuh"
 
 namespace sherry {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------------------
 // Few rows: mma.sync on fragments decoded in registers
@@ -32,22 +18,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 // results do not depend on timing).  One warp copies pages into a ring (a page's keys and values
 // are one contiguous block: one bulk copy); four warps take 16 of a page's tokens each.  The
 // product is S^T = K q^T with 16 tokens by 8 rows: the 8-wide side carries the few rows, so
-// 4 query heads per key/value head fill half of the instruction instead of a quarter.
+// 4 query heads per key/value head fill half of the instruction instead of a quarter.  The 128 of
+// the codes' bf16 is taken out of the first product by starting it at -128 sum(q), and out of the
+// second by -136 times the sum of the rounded p s.
 constexpr int kFewWarps = 4;
 constexpr int kFewThreads = 32 * (kFewWarps + 1);
 constexpr int kFewCtasMax = 1024;  // bounds the workspace
-
-struct FewParams {
-    Kv4View c;
-    const uint16_t *q;
-    uint16_t *out;
-    float *ws;          // [2 grid][rows][D], then [2 grid][rows] pairs (m, l)
-    long long q_stride, out_stride;
-    int g;              // query heads per key/value head
-    int grid;
-    float scale2;       // scale * log2(e)
-    unsigned int *err;
-};
+constexpr int kFewRows = 32;       // rows of a sequence up to which this kernel takes it
 
 template <int D, int NT>
 struct Few {
@@ -65,30 +42,33 @@ struct SeqWork {
 };
 
 template <int ROWS>
-__device__ __forceinline__ SeqWork seq_work(const Kv4View &c, int b, int g) {
+__device__ __forceinline__ SeqWork seq_work(const AttnParams &p, int b) {
+    const Kv4View &c = p.c;
+    const int g = p.g;
     SeqWork s;
     int n;
     kv4_rows(c, b, s.first, n);
     s.rows = n;
     s.len = max(__ldg(c.lens + b), 0);
-    s.tiles = (int)(((long long)n * g + ROWS - 1) / ROWS);
+    const long long rows = (long long)n * g;
+    s.tiles = rows > p.few_rows ? 0 : (int)((rows + ROWS - 1) / ROWS);
     // an empty sequence has one page without keys: its rows are written as zeros
     s.pages = max((min(s.len, c.width * SHERRY_KV4_PAGE) + SHERRY_KV4_PAGE - 1) / SHERRY_KV4_PAGE, 1);
     return s;
 }
 
 template <int ROWS>
-__device__ __forceinline__ long long seq_units(const Kv4View &c, int b, int g) {
-    if (b >= c.B) return 0;
-    const SeqWork s = seq_work<ROWS>(c, b, g);
-    return (long long)c.H * s.tiles * s.pages;
+__device__ __forceinline__ long long seq_units(const AttnParams &p, int b) {
+    if (b >= p.c.B) return 0;
+    const SeqWork s = seq_work<ROWS>(p, b);
+    return (long long)p.c.H * s.tiles * s.pages;
 }
 
 // Sum of the batch's units (every lane of a full warp).
 template <int ROWS>
-__device__ long long all_units(const Kv4View &c, int g) {
+__device__ long long all_units(const AttnParams &p) {
     long long sum = 0;
-    for (int b = threadIdx.x & 31; b < c.B; b += 32) sum += seq_units<ROWS>(c, b, g);
+    for (int b = threadIdx.x & 31; b < p.c.B; b += 32) sum += seq_units<ROWS>(p, b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     return sum;
@@ -96,11 +76,11 @@ __device__ long long all_units(const Kv4View &c, int g) {
 
 // The sequence that holds unit w (w below all_units) and the units before it.
 template <int ROWS>
-__device__ void find_unit(const Kv4View &c, int g, long long w, int &b, long long &before) {
+__device__ void find_unit(const AttnParams &p, long long w, int &b, long long &before) {
     const int lane = threadIdx.x & 31;
     long long base = 0;
-    for (int b0 = 0; b0 < c.B; b0 += 32) {
-        const long long mine = seq_units<ROWS>(c, b0 + lane, g);
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+        const long long mine = seq_units<ROWS>(p, b0 + lane);
         long long sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -116,7 +96,7 @@ __device__ void find_unit(const Kv4View &c, int g, long long w, int &b, long lon
         }
         base += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    b = c.B;
+    b = p.c.B;
     before = base;
 }
 
@@ -132,19 +112,19 @@ struct Walk {
     SeqWork s;
     int h, tile, page0, page1;
 
-    __device__ __forceinline__ void start(const Kv4View &c, int g, long long from, long long to) {
+    __device__ __forceinline__ void start(const AttnParams &p, long long from, long long to) {
         w = from;
         end = to;
-        find_unit<ROWS>(c, g, w, b, before);
-        if (b < c.B) s = seq_work<ROWS>(c, b, g);
+        find_unit<ROWS>(p, w, b, before);
+        if (b < p.c.B) s = seq_work<ROWS>(p, b);
     }
     // The next piece: pages [page0, page1) of (b, h, tile); false at the end.
-    __device__ __forceinline__ bool next(const Kv4View &c, int g) {
+    __device__ __forceinline__ bool next(const AttnParams &p) {
         if (w >= end) return false;
-        while (w - before >= (long long)c.H * s.tiles * s.pages) {
-            before += (long long)c.H * s.tiles * s.pages;
-            if (++b >= c.B) return false;
-            s = seq_work<ROWS>(c, b, g);
+        while (w - before >= (long long)p.c.H * s.tiles * s.pages) {
+            before += (long long)p.c.H * s.tiles * s.pages;
+            if (++b >= p.c.B) return false;
+            s = seq_work<ROWS>(p, b);
         }
         const long long u = w - before;
         const int unit = (int)(u / s.pages);
@@ -171,25 +151,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return d;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Low nibbles of both halves as two bf16 128 + c.
-__device__ __forceinline__ uint32_t code_pair(uint32_t x) { return (x & 0x000F000Fu) | 0x43004300u; }
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
 // Barrier of the consumer warps alone.
 __device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory"); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_constant__ AttnParams p) {
     using F = Few<D, NT>;
     constexpr int kRows = F::kRows, kS = F::kStages, MT = D / 16, WK = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -210,23 +176,23 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");  // lengths and cache come from the kernels before
-    const long long W = all_units<kRows>(p.c, p.g);
+    const long long W = all_units<kRows>(p);
     const int n = (int)min((long long)p.grid, W);
     if ((int)blockIdx.x >= n) return;
     const long long from = run_start(W, blockIdx.x, n), to = run_start(W, blockIdx.x + 1, n);
     Walk<kRows> walk;
-    walk.start(p.c, p.g, from, to);
+    walk.start(p, from, to);
 
     if (warp == kFewWarps) {
         // ---------------- copies ----------------
         if (lane == 0) {
             uint32_t it = 0;
-            while (walk.next(p.c, p.g)) {
+            while (walk.next(p)) {
                 if (walk.s.len > p.c.width * SHERRY_KV4_PAGE) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
                 for (int pg = walk.page0; pg < walk.page1; pg++, it++) {
                     const int s = it % kS;
                     // where a wait gives up, the rest of the walk waits no more and copies nothing
-                    const bool ok = mbar_wait(empty + s, ((it / kS) & 1) ^ 1, abort, p.err) && !*(volatile int *)abort;
+                    const bool ok = mbar_wait(empty + s, ((it / kS) & 1) ^ 1, abort, p.err, p.wait_limit) && !*(volatile int *)abort;
                     int page = -1;
                     if (ok && walk.s.len > 0) page = kv4_page(p.c, walk.b, pg * SHERRY_KV4_PAGE, p.err);
                     there[s] = page >= 0;
@@ -253,7 +219,7 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
     const int tok_r = r ^ (r >> 2 & 1);                       // rows r and r + 8 (+ 8)
     const int tok_v0 = (2 * c) ^ (c >> 1 & 1), tok_v1 = (2 * c + 1) ^ (c >> 1 & 1);
     uint32_t it = 0;
-    while (walk.next(p.c, p.g)) {
+    while (walk.next(p)) {
         const int nrow = walk.s.rows * p.g, row0 = walk.tile * kRows;
         const int pos0 = walk.s.len - walk.s.rows;            // position of the first new token
         // q: lane (r, c) holds elements [c D / 4, (c + 1) D / 4) of row r of each row group
@@ -310,7 +276,7 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
         }
         for (int pg = walk.page0; pg < walk.page1; pg++, it++) {
             const int s = it % kS;
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, (it / kS) & 1, abort, p.err));
+            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, (it / kS) & 1, abort, p.err, p.wait_limit));
             const int t0 = pg * SHERRY_KV4_PAGE + 16 * warp;  // first token of this warp's tile
             if (ok && there[s] && t0 <= last_max) {
                 const uint8_t *kb = smem + s * F::kStage, *vb = kb + Kv4<D>::kBlock;
@@ -531,78 +497,68 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
     }
 }
 
-// Joins the parts of the row tiles that were cut: one CTA per (row, key/value head), one warp per
-// query head of it, the parts in the order of the CTAs.
-constexpr int kJoinThreads = 128;
-
+// Joins the parts of the row tiles that the runs cut: CTA i takes the one that begins in run i and
+// goes on in the next, one warp per row, its parts in the order of the CTAs.
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ FewParams p) {
+__global__ void __launch_bounds__(256 * NT, 2) attn_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kRows = 8 * NT, E = D / 32;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
-    int b, pos;
-    if (!kv4_find(p.c, t, b, pos)) return;
-    const SeqWork s = seq_work<kRows>(p.c, b, p.g);
-    long long before = 0, W = 0;
-    for (int i = lane; i < p.c.B; i += 32) {
-        const long long u = seq_units<kRows>(p.c, i, p.g);
-        W += u;
-        if (i < b) before += u;
-    }
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const long long W = all_units<kRows>(p);
+    const int n = (int)min((long long)p.grid, W), i0 = blockIdx.x;
+    if (i0 >= n - 1) return;
+    const long long from = run_start(W, i0, n), to = run_start(W, i0 + 1, n);
+    int b;
+    long long before;
+    find_unit<kRows>(p, to - 1, b, before);
+    if (b >= p.c.B) return;
+    const SeqWork s = seq_work<kRows>(p, b);
+    const int unit = (int)((to - 1 - before) / s.pages);
+    const long long w0 = before + (long long)unit * s.pages, w1 = w0 + s.pages;
+    if (w1 <= to || w0 < from) return;  // not cut here, or begun by an earlier CTA
+    const int h = unit / s.tiles, rw = (unit - h * s.tiles) * kRows + row;
+    if (rw >= s.rows * p.g) return;
+    const int i1 = run_of(W, w1 - 1, n);
+    const float2 *ml = reinterpret_cast<const float2 *>(p.ws + 2LL * p.grid * kRows * D);
+    const int first_slot = w0 > from ? 1 : 0;
+    float m = -INFINITY;
+    for (int i = i0 + lane; i <= i1; i += 32) m = fmaxf(m, ml[(2LL * i + (i == i0 ? first_slot : 0)) * kRows + row].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        W += __shfl_xor_sync(0xFFFFFFFFu, W, o);
-        before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-    }
-    const int n = (int)min((long long)p.grid, W);
-    for (int j = threadIdx.x >> 5; j < p.g; j += kJoinThreads / 32) {
-        const int rw = (t - s.first) * p.g + j, row = rw % kRows;
-        const long long w0 = before + ((long long)h * s.tiles + rw / kRows) * s.pages;
-        const int i0 = run_of(W, w0, n), i1 = run_of(W, w0 + s.pages - 1, n);
-        if (i0 == i1) continue;  // one CTA held all of it and wrote the result
-        const float2 *ml = reinterpret_cast<const float2 *>(p.ws + 2LL * p.grid * kRows * D);
-        const int first_slot = w0 > run_start(W, i0, n) ? 1 : 0;
-        float m = -INFINITY;
-        for (int i = i0 + lane; i <= i1; i += 32)
-            m = fmaxf(m, ml[(2LL * i + (i == i0 ? first_slot : 0)) * kRows + row].x);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float l = 0.0f, acc[E];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        float l = 0.0f, acc[E];
-#pragma unroll
-        for (int e = 0; e < E; e++) acc[e] = 0.0f;
-        for (int ib = i0; ib <= i1; ib += 32) {
-            const int i = ib + lane;
-            float f = 0.0f;
-            if (i <= i1) {
-                const float2 v = ml[(2LL * i + (i == i0 ? first_slot : 0)) * kRows + row];
-                // a part without keys has sum 0; a NaN among its scores shows in the sum
-                f = v.x == -INFINITY ? (v.y == 0.0f ? 0.0f : v.y) : exp2_fast(v.x - m);
-                l += v.y * f;
-            }
-            const int k1 = min(32, i1 - ib + 1);
-#pragma unroll 4
-            for (int k = 0; k < k1; k++) {
-                const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-                const long long slot = 2LL * (ib + k) + (ib + k == i0 ? first_slot : 0);
-                const float *src = p.ws + (slot * kRows + row) * D + lane * E;
-                if (E == 2) {
-                    const float2 v = *reinterpret_cast<const float2 *>(src);
-                    acc[0] += fk * v.x, acc[1] += fk * v.y;
-                } else {
-                    const float4 v = *reinterpret_cast<const float4 *>(src);
-                    acc[0] += fk * v.x, acc[1] += fk * v.y, acc[E - 2] += fk * v.z, acc[E - 1] += fk * v.w;
-                }
+    for (int e = 0; e < E; e++) acc[e] = 0.0f;
+    for (int ib = i0; ib <= i1; ib += 32) {
+        const int i = ib + lane;
+        float f = 0.0f;
+        if (i <= i1) {
+            const float2 v = ml[(2LL * i + (i == i0 ? first_slot : 0)) * kRows + row];
+            // a part without keys has sum 0; a NaN among its scores shows in the sum
+            f = v.x == -INFINITY ? (v.y == 0.0f ? 0.0f : v.y) : exp2_fast(v.x - m);
+            l += v.y * f;
+        }
+        const int k1 = min(32, i1 - ib + 1);
+#pragma unroll 8
+        for (int k = 0; k < k1; k++) {
+            const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
+            const long long slot = 2LL * (ib + k) + (ib + k == i0 ? first_slot : 0);
+            const float *src = p.ws + (slot * kRows + row) * D + lane * E;
+            if (E == 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(src);
+                acc[0] += fk * v.x, acc[1] += fk * v.y;
+            } else {
+                const float4 v = *reinterpret_cast<const float4 *>(src);
+                acc[0] += fk * v.x, acc[1] += fk * v.y, acc[E - 2] += fk * v.z, acc[E - 1] += fk * v.w;
             }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t *dst = p.out + (long long)t * p.out_stride + (long long)(h * p.g + j) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint16_t *dst = p.out + (long long)(s.first + rw / p.g) * p.out_stride + (long long)(h * p.g + rw % p.g) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
 }
 
 // Blocks per SM of the kernel, with its shared-memory attribute set, once per device and context.
@@ -624,7 +580,7 @@ int few_blocks_per_sm(K kernel, size_t smem, OccupancyCache &cache) {
 }
 
 template <typename K>
-void launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const FewParams &p) {
+void launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const AttnParams &p) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
@@ -639,7 +595,7 @@ void launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st
 }
 
 template <int D, int NT>
-sherry_status few_launch(FewParams p, cudaStream_t stream) {
+sherry_status few_launch(AttnParams p, cudaStream_t stream) {
     using F = Few<D, NT>;
     static OccupancyCache cache;
     const int bps = few_blocks_per_sm(attn_few_kernel<D, NT>, F::kSmem, cache);
@@ -648,7 +604,7 @@ sherry_status few_launch(FewParams p, cudaStream_t stream) {
     const sherry_status st = launch_status("sherry_attn_kv4");
     // a table of one page cuts nothing
     if (st != SHERRY_OK || p.c.width == 1) return st;
-    launch_after(attn_join_kernel<D, NT>, dim3((unsigned)p.c.T, (unsigned)p.c.H), kJoinThreads, 0, stream, p);
+    launch_after(attn_join_kernel<D, NT>, dim3((unsigned)p.grid), 256 * NT, 0, stream, p);
     return launch_status("sherry_attn_kv4 (join)");
 }
 
@@ -676,7 +632,7 @@ extern "C" sherry_status sherry_attn_kv4(const sherry_kv4 *c, const uint16_t *q,
     if (!workspace) return SHERRY_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return SHERRY_ERR_ALIGN;
     if (workspace_bytes < sherry_attn_kv4_workspace_bytes(c->T, Hq, c->D)) return SHERRY_ERR_WORKSPACE;
-    FewParams p;
+    AttnParams p;
     p.c = kv4_view(c);
     p.q = q;
     p.out = out;
@@ -689,8 +645,16 @@ extern "C" sherry_status sherry_attn_kv4(const sherry_kv4 *c, const uint16_t *q,
     p.err = kv4_error_address();
     if (!p.err) return SHERRY_ERR_CUDA;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t most = c->cu_q ? (max_q > 0 ? max_q : c->T) : 1;
-    const bool few = most * p.g <= 8;
-    if (c->D == 64) return few ? few_launch<64, 1>(p, s) : few_launch<64, 2>(p, s);
-    return few ? few_launch<128, 1>(p, s) : few_launch<128, 2>(p, s);
+    const int64_t most = (c->cu_q ? (max_q > 0 ? std::min(max_q, c->T) : c->T) : 1) * p.g;  // rows of a sequence
+    p.wait_limit = wait_limit();
+    p.few_rows = 0x7FFFFFFF;
+    if (most > kFewRows) {
+        // a batch may hold both kinds; a lone sequence is one or the other
+        p.few_rows = c->B == 1 ? -1 : kFewRows;
+        st = attn_tile_launch(p, c->D, s);
+        if (st != SHERRY_OK || c->B == 1) return st;
+    }
+    const bool one = most <= 8;
+    if (c->D == 64) return one ? few_launch<64, 1>(p, s) : few_launch<64, 2>(p, s);
+    return one ? few_launch<128, 1>(p, s) : few_launch<128, 2>(p, s);
 }

@@ -434,6 +434,13 @@ sherry_status gemm_launch(const uint32_t *codes, const float *scales, const int8
 }  // namespace
 }  // namespace sherry
 
+namespace sherry {
+long long wait_limit() {
+    const long long lim = g_wait_limit.load(std::memory_order_relaxed);
+    return lim > 0 ? lim : kDefaultWaitLimit;
+}
+}  // namespace sherry
+
 extern "C" sherry_status sherry_gemm(const uint32_t *codes, const float *scales, const int8_t *x,
                                      float *y, int64_t M, int64_t N, int64_t K,
                                      sherry_stream_t stream) {

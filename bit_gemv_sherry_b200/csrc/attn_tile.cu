@@ -3,18 +3,30 @@
 //
 // A CTA takes 256 rows of one key/value head, as two tiles of 128, so that each decoded key and
 // value serves both (and all query heads of the group: a row is a new token and a query head).
-// Per 128 tokens:
-//     S = Q C_k^T        codes c - 8 as bf16, K-major, in shared memory; S in tensor memory
-//     x = s_k S + (m_k + 8 s_k) sum(q)      (times scale log2 e), masked at the diagonal only
-//     P = bf16(2^(x - m) s_v) back into S's tensor memory, the A operand of
-//     O += P C_v         codes transposed to [D][tokens], so that both operands are K-major
-// and in fp32 registers  l += sum p,  corr += sum p (m_v + 8 s_v);  out = (O + corr) / l.
+// Per step of 128 tokens:
+//     S = Q K^T            fp16 operands, K-major, in shared memory; S (fp32) in tensor memory
+//     P = fp16(2^(f S - m))  back into S's tensor memory, the A operand of
+//     O += P V             V transposed to [D][tokens], so that both operands are K-major
+// and l += sum p in fp32;  out = O / l.
+// Precision: decoded values are m + s c rounded once to fp16 (11 bits; bf16's 8 would cost the
+// scores of a peaked softmax several percent), after a division by a power of two that brings the
+// largest to about 2^-7: per page for keys (f takes it back), one running power for values (O is
+// rescaled when it has to grow).  There a code's bits are themselves an fp16, c 2^-24, and one FMA
+// makes the value.  Queries are bf16: a power of two per row makes them exact in fp16.
+// Probabilities are fp16 of values up to 2^15, the row's maximum at 2^10 or above: relative 2^-11
+// down to 2^-24 of the largest.
+// Earlier forms, per step with heads of 128: codes as operands and steps and low ends applied to S
+// and P by the softmax threads, whose scales came from shared memory (8,000 clocks: 128 16-byte
+// loads a row in the way of the products' operand reads); unrolled over the whole step (7,000:
+// four roles' straight-line code does not fit the instruction cache, every role ran at six clocks
+// an instruction).
 // Roles: warps 0-3 and 4-7 the softmax of a tile each (a thread owns a row: no shuffles), warps
-// 8-9 decode keys, 10-11 values, warp 12 issues the products.  The tiles alternate: while one's
-// softmax runs, the tensor cores work for the other.
-// The bound is shared by the exponentials (16 a clock and SM: 2048 clocks per 256 x 128 scores),
-// the products (1024 clocks for heads of 64, 2048 for 128) and the issue of about six
-// instructions per score in 64-bit pairs.
+// 8-9 decode keys, 10-11 values, warp 12 issues the products, 13 copies pages (codes of keys and
+// values of a page are one bulk copy).  The tiles alternate: while one's softmax runs, the tensor
+// cores work for the other.
+// The bounds: the exponentials (16 a clock and SM: 2048 clocks per 256 x 128 scores), the products
+// (1024 clocks for heads of 64, 2048 for 128) and shared memory (decoded operands written once and
+// read by the products: 1152 and 2048 clocks at 128 bytes a clock).
 #include <algorithm>
 
 #include "attn.cuh"
@@ -25,8 +37,9 @@ namespace {
 constexpr int kRowsTile = 128;
 constexpr int kRowsCta = 2 * kRowsTile;
 constexpr int kKeys = 128;                 // tokens per step: two pages
-constexpr int kTileThreads = 13 * 32;
-constexpr int kScaleSlots = 4;
+constexpr int kTileThreads = 14 * 32;
+constexpr int kInfoSlots = 4;
+constexpr float kUp = 10.0f;               // a probability of 1 is held as 2^10
 constexpr int kAllSeen = 0x7FFFFFFF - 2 * kKeys;
 constexpr int kTmemCols = 512;             // S0, S1 (128 columns each), O0, O1 (D each)
 constexpr long long kDrainLimit = 1000000000LL;
@@ -35,25 +48,33 @@ template <int D>
 struct Tile {
     static constexpr int kQ = kRowsTile * D * 2;      // one tile's queries
     static constexpr int kOp = kKeys * D * 2;         // decoded keys or values of a step
-    static constexpr int kScales = kScaleSlots * 4 * kKeys * 4;
-    static constexpr int kBars = 256;
-    // one CTA per SM in any case (its tensor memory), so heads of 64 ask for as much as keeps
-    // a second one away
-    static constexpr size_t kUse = 2 * kQ + 4 * kOp + kScales + kBars + 1024;
+    static constexpr int kPage = 2 * Kv4<D>::kBlock;  // a page of a head, as it is in the cache
+    static constexpr int kBars = 512;
+    // One CTA per SM in any case (its tensor memory), so heads of 64 ask for as much as keeps a second
+    // one away.  No room is left for aligning the operands: the base is at 1024 (checked).
+    static constexpr size_t kUse = 2 * kQ + 4 * kOp + 4 * kPage + kBars;
     static constexpr size_t kSmem = kUse < 120 * 1024 ? 120 * 1024 : kUse;
 };
 
-// D = fp32, A and B = bf16, both K-major, 128 x N
+// D = fp32, A and B = fp16, both K-major, 128 x N
 template <int N>
-constexpr uint32_t kIdescBf16 = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
-                                ((uint32_t)(kRowsTile >> 4) << 24);
+constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRowsTile >> 4) << 24);
+
+// What the softmax has to know of a step.
+struct StepInfo {
+    float key_scale[2];   // a key of the first, second page is its fp16 value times this
+    int value_exp;        // a value is its fp16 value times 2^value_exp
+    int there;            // bit 0, 1: the first, second page is in the cache
+    uint32_t bad[4];      // tokens 32 i + bit whose value is NaN
+};
 
 struct TileBars {
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[kScaleSlots];
-    uint64_t s_full[2], p_full[2], o_full[2], drain;
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], info_full[kInfoSlots];
+    uint64_t s_full[2], p_full[2], o_full[2], raw_full[2], raw_empty[2], drain;
     uint32_t tmem;
     int abort;
-    int there[kScaleSlots];  // bit 0, 1: the step's first, second page is in the cache
+    int there[2];            // of the raw pages
+    StepInfo info[kInfoSlots];
 };
 
 // ---- pairs of fp32 ----
@@ -74,22 +95,125 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ f2 add2(f2 a, f2 b) {
     f2 d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 
-// Two codes as bf16 c - 8.
-__device__ __forceinline__ uint32_t code_pair8(uint32_t x) {
+// tmem_ld_wait that the loaded registers depend on: nothing that reads them moves above it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// 2^e for any e (0 or the largest power where that is out of range).
+__device__ __forceinline__ float pow2(int e) {
+    return e < -126 ? (e < -149 ? 0.0f : __int_as_float(1 << (e + 149))) : __int_as_float((min(e, 127) + 127) << 23);
+}
+
+// Power of two to divide by so that magnitudes up to `most` become at most 2^(bits + 1).
+__device__ __forceinline__ int exp_for(float most, int bits) {
+    return max((int)(__float_as_uint(most) >> 23) - 127 - bits, -100);  // most >= 0 and finite
+}
+
+// Two values m + s c, c the nibbles of x that MASK names, read as fp16 (c 2^-24, or c 2^-20 for the
+// nibbles one up): s is the step times 2^24 or 2^20 to match.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t value_pair(uint32_t x, uint32_t s, uint32_t m) {
     uint32_t d;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(code_pair(x)), "r"(0x43084308u));
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x & MASK), "r"(s), "r"(m));
     return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// A pair (step, low end) whose values are finite and can be ordered: magnitude bound of its values,
+// 0 where it is not.
+__device__ __forceinline__ float pair_most(uint32_t sm) {
+    const float v = fmaxf(fabsf(kv4_low(sm)), fabsf(kv4_low(sm) + 15.0f * kv4_step(sm)));
+    return v < INFINITY ? v : 0.0f;
+}
+__device__ __forceinline__ bool pair_bad(uint32_t sm) {
+    return !(fabsf(kv4_low(sm)) < INFINITY && fabsf(kv4_low(sm) + 15.0f * kv4_step(sm)) < INFINITY);
+}
+
+// Maximum of non-negative floats over a warp.
+__device__ __forceinline__ float warp_max(float v) {
+    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// One k-step of 16.  Operands are low descriptor words (address / 16) and constant offsets, put
+// together where they are used: 64-bit descriptors kept ready for 32 k-steps would spill.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, version 1, 128-byte swizzle
+template <int A, int B>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "add.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\t"
+        "mov.b64 da, {x, %7};\n\tmov.b64 db, {y, %7};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(A), "n"(B), "r"(kDescHigh)
+        : "memory");
+}
+template <int A, int B>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "add.u32 x, %1, %5;\n\tadd.u32 y, %2, %6;\n\t"
+        "mov.b64 db, {y, %7};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(A), "n"(B), "r"(kDescHigh)
+        : "memory");
+}
+template <int K, int N, int ROWS>
+__device__ __forceinline__ void mma_ss_all(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    if constexpr (K < N) {
+        constexpr int off = ((K / 4) * (ROWS * 128) + (K & 3) * 32) >> 4;
+        mma_ss<off, off>(d, a, b, idesc, K != 0);
+        mma_ss_all<K + 1, N, ROWS>(d, a, b, idesc);
+    }
+}
+template <int K, int N, int ROWS>
+__device__ __forceinline__ void mma_ts_all(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    if constexpr (K < N) {
+        mma_ts<8 * K, (((K / 4) * (ROWS * 128) + (K & 3) * 32) >> 4)>(d, a, b, idesc, K != 0 ? 1u : acc);
+        mma_ts_all<K + 1, N, ROWS>(d, a, b, idesc, acc);
+    }
+}
+
+// One arrival for a warp's work: 32 lanes on one barrier are 32 atomics in a row, in the way of the
+// products' operand reads (a step of heads of 128 took 7,600 clocks instead of 5,000).
+__device__ __forceinline__ void warp_arrive(uint64_t *b) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(b);
+}
+
+// mbar_wait by a whole warp; its lanes go on together.
+__device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort, unsigned int *err,
+                                          long long limit) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(b, parity, abort, err, limit));
 }
 
 // A row tile's place in the batch.
@@ -131,93 +255,85 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int i, Place &w) 
     return false;
 }
 
-// One thread's row over one step of 128 tokens.
-struct RowState {
-    float m, l;      // reference of the exponentials, sum
-    float corr;      // sum p (m_v + 8 s_v)
-};
+// 32 lanes x 32 bit, 16 consecutive columns: thread t writes lane (base + t).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+        " %16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 
-// Largest score of the row in this step (-inf if none is seen).
-__device__ __forceinline__ float step_max(uint32_t s_tmem, const float *sc, float qsum, int seen, int there) {
-    float mx = -INFINITY;
+// Largest score of the row in this step (-inf if none is seen); f0, f1 >= 0 scale the pages' scores.
+// MASK: the row sees the step's first `seen` tokens, of pages that are there.
+template <bool MASK>
+__device__ __forceinline__ float step_max(uint32_t s_tmem, float f0, float f1, int seen, int there) {
+    float page[2];
 #pragma unroll 1
     for (int c0 = 0; c0 < kKeys; c0 += 32) {
         uint32_t r[32];
         tmem_ld32(s_tmem + c0, r);
-        tmem_ld_wait();
+        tmem_ld_wait32(r);
+        const int n = MASK ? (there >> (c0 / SHERRY_KV4_PAGE) & 1 ? seen - c0 : 0) : 32;
+        float m[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) m[k] = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 32; i++) {
-            const float x = sc[c0 + i] * __uint_as_float(r[i]) + sc[kKeys + c0 + i] * qsum;
-            const bool ok = c0 + i < seen && (there >> ((c0 + i) / SHERRY_KV4_PAGE) & 1);
-            mx = fmaxf(mx, ok ? x : -INFINITY);
+            const float v = __uint_as_float(r[i]);
+            m[i & 3] = fmaxf(m[i & 3], !MASK || i < n ? v : -INFINITY);
         }
+        const float v = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        if (c0 == 0) page[0] = v;
+        else if (c0 == 32) page[0] = fmaxf(page[0], v);
+        else if (c0 == 64) page[1] = v;
+        else page[1] = fmaxf(page[1], v);
     }
-    return mx;
+    // 0 * -inf would be NaN
+    const float a = page[0] == -INFINITY ? page[0] : f0 * page[0], b = page[1] == -INFINITY ? page[1] : f1 * page[1];
+    return fmaxf(a, b);
 }
 
-// Probabilities of the step against the reference m, packed for the second product; sum and corr of
-// the step alone.  MASK: the row sees the step's first `seen` tokens, of pages that are there.
+// P = 2^(f S - ref) of the step as fp16 into the tensor memory of S (the columns that are read
+// already), and their sum.
 template <bool MASK>
-__device__ __forceinline__ void step_probs(uint32_t s_tmem, const float *sc, float qsum, float ref, int seen, int there,
-                                           uint32_t (&pk)[64], float &sum, float &corr) {
-    const f2 q2 = pair2(qsum, qsum), nm = pair2(-ref, -ref);
-    f2 sum2 = pair2(0.0f, 0.0f), corr2 = sum2;
-#pragma unroll
+__device__ __forceinline__ float step_probs(uint32_t s_tmem, float f0, float f1, float ref, int seen, int there) {
+    const f2 nm = pair2(-ref, -ref);
+    f2 sum2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
+#pragma unroll 1
     for (int c0 = 0; c0 < kKeys; c0 += 32) {
-        uint32_t r[32];
+        uint32_t r[32], pk[16];
         tmem_ld32(s_tmem + c0, r);
-        tmem_ld_wait();
+        tmem_ld_wait32(r);
+        const float fp = c0 < SHERRY_KV4_PAGE ? f0 : f1;
+        const f2 f = pair2(fp, fp);
+        const int n = MASK ? (there >> (c0 / SHERRY_KV4_PAGE) & 1 ? seen - c0 : 0) : 32;
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const ulonglong2 sk = *reinterpret_cast<const ulonglong2 *>(sc + c0 + i);
-            const ulonglong2 mk = *reinterpret_cast<const ulonglong2 *>(sc + kKeys + c0 + i);
-            const ulonglong2 sv = *reinterpret_cast<const ulonglong2 *>(sc + 2 * kKeys + c0 + i);
-            const ulonglong2 cv = *reinterpret_cast<const ulonglong2 *>(sc + 3 * kKeys + c0 + i);
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const int t = c0 + i + 2 * k;
-                const f2 y = fma2(k ? sk.y : sk.x, pair2u(r[i + 2 * k], r[i + 2 * k + 1]), fma2(k ? mk.y : mk.x, q2, nm));
-                float ya, yb;
-                split2(y, ya, yb);
-                bool oka = true, okb = true;
-                if (MASK) {
-                    const bool pg = there >> (t / SHERRY_KV4_PAGE) & 1;
-                    oka = pg && t < seen;
-                    okb = pg && t + 1 < seen;
-                }
-                const float pa = oka ? exp2_fast(ya) : 0.0f, pb = okb ? exp2_fast(yb) : 0.0f;
-                const f2 p2 = pair2(pa, pb);
-                sum2 = add2(sum2, p2);
-                f2 sv2 = k ? sv.y : sv.x, cv2 = k ? cv.y : cv.x;
-                if (MASK) {  // a token that is not seen may hold anything, NaN too
-                    float a, b;
-                    split2(sv2, a, b);
-                    sv2 = pair2(oka ? a : 0.0f, okb ? b : 0.0f);
-                    split2(cv2, a, b);
-                    cv2 = pair2(oka ? a : 0.0f, okb ? b : 0.0f);
-                }
-                corr2 = fma2(p2, cv2, corr2);
-                float a, b;
-                split2(mul2(p2, sv2), a, b);
-                pk[t / 2] = pack_bf16(a, b);
+        for (int i = 0; i < 32; i += 2) {
+            float a, b;
+            split2(fma2(f, pair2u(r[i], r[i + 1]), nm), a, b);
+            a = exp2_fast(a);
+            b = exp2_fast(b);
+            if (MASK) {
+                a = i < n ? a : 0.0f;
+                b = i + 1 < n ? b : 0.0f;
             }
+            sum2[(i / 2) & 1] = add2(sum2[(i / 2) & 1], pair2(a, b));
+            pk[i / 2] = pack_f16(a, b);
         }
+        tmem_st16(s_tmem + c0 / 2, pk);
     }
     float a, b;
-    split2(sum2, a, b);
-    sum = a + b;
-    split2(corr2, a, b);
-    corr = a + b;
+    split2(add2(sum2[0], sum2[1]), a, b);
+    return a + b;
 }
 
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid_constant__ AttnParams p) {
     using T = Tile<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *sq = smem, *sk = sq + 2 * T::kQ, *sv = sk + 2 * T::kOp;
-    float *scales = reinterpret_cast<float *>(sv + 2 * T::kOp);  // [slot][s_k, m_k, s_v, m_v][128]
-    TileBars *bar = reinterpret_cast<TileBars *>(reinterpret_cast<uint8_t *>(scales) + T::kScales);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *sq = smem, *sk = sq + 2 * T::kQ, *sv = sk + 2 * T::kOp, *raw = sv + 2 * T::kOp;
+    TileBars *bar = reinterpret_cast<TileBars *>(raw + 4 * T::kPage);
     static_assert(sizeof(TileBars) <= T::kBars, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -231,19 +347,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     const int keys = min(pos0 + hi_row / p.g + 1, p.c.width * SHERRY_KV4_PAGE);
     const int steps = keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
     const long long limit = p.wait_limit;
+    if (smem_u32(smem) & 1023) {  // the swizzled operands need it
+        if (threadIdx.x == 0) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_UNSUPPORTED);
+        return;
+    }
 
     if (threadIdx.x == 0) {
-        mbar_init(&bar->q_full, kRowsCta);
+        mbar_init(&bar->q_full, 8);
         for (int i = 0; i < 2; i++) {
-            mbar_init(&bar->k_full[i], 64);
-            mbar_init(&bar->v_full[i], 64);
+            mbar_init(&bar->k_full[i], 2);
+            mbar_init(&bar->v_full[i], 2);
             mbar_init(&bar->k_empty[i], 1);
             mbar_init(&bar->v_empty[i], 1);
             mbar_init(&bar->s_full[i], 1);
-            mbar_init(&bar->p_full[i], kRowsTile);
+            mbar_init(&bar->p_full[i], 4);
             mbar_init(&bar->o_full[i], 1);
+            mbar_init(&bar->raw_full[i], 1);
+            mbar_init(&bar->raw_empty[i], 4);
         }
-        for (int i = 0; i < kScaleSlots; i++) mbar_init(&bar->sc_full[i], 128);
+        for (int i = 0; i < kInfoSlots; i++) mbar_init(&bar->info_full[i], 4);
         mbar_init(&bar->drain, 1);
         bar->abort = 0;
         if (w.len > p.c.width * SHERRY_KV4_PAGE) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
@@ -268,103 +390,110 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         const int lo_row = row0 + i * kRowsTile;
         const int last_min = lo_row < nrow ? pos0 + lo_row / p.g : kAllSeen;
         // queries to shared memory (elements of each eight in the order 0 4 1 5 2 6 3 7, as the codes
-        // come out of their words), K-major with 128-byte rows swizzled
-        float qsum = 0.0f;
+        // come out of their words), K-major with 128-byte rows swizzled, as fp16 of q 2^-qe
+        float row_scale;
         {
             const uint16_t *src = p.q + (long long)(w.first + rw / p.g) * p.q_stride + (long long)(h * p.g + rw % p.g) * D;
             uint8_t *dst = sq + i * T::kQ + r * 128;
-#pragma unroll
+            float most = 0.0f;
+#pragma unroll 4
             for (int c = 0; c < D / 8; c++) {
                 uint4 u = make_uint4(0, 0, 0, 0);
                 if (live) u = *reinterpret_cast<const uint4 *>(src + 8 * c);
                 const uint32_t e[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    qsum += __uint_as_float(e[k] << 16) + __uint_as_float(e[k] & 0xFFFF0000u);
-                const uint4 v = make_uint4(prmt(u.x, u.z, 0x5410), prmt(u.x, u.z, 0x7632), prmt(u.y, u.w, 0x5410),
-                                           prmt(u.y, u.w, 0x7632));
-                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRowsTile * 128) + (((c & 7) ^ (r & 7)) << 4)) = v;
+                    most = fmaxf(most, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
+            }
+            const int qe = exp_for(fminf(most, 3e38f), 7);
+            const float down = copysignf(pow2(-qe), p.scale2);  // scores come out with the scale's sign
+            row_scale = fabsf(p.scale2) * pow2(qe);
+#pragma unroll 4
+            for (int c = 0; c < D / 8; c++) {
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (live) u = *reinterpret_cast<const uint4 *>(src + 8 * c);
+                const uint32_t lo[2] = {u.x, u.y}, hi[2] = {u.z, u.w};
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    v[2 * k] = pack_f16(__uint_as_float(lo[k] << 16) * down, __uint_as_float(hi[k] << 16) * down);
+                    v[2 * k + 1] = pack_f16(__uint_as_float(lo[k] & 0xFFFF0000u) * down, __uint_as_float(hi[k] & 0xFFFF0000u) * down);
+                }
+                *reinterpret_cast<uint4 *>(dst + (c / 8) * (kRowsTile * 128) + (((c & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bar->q_full);
+        warp_arrive(&bar->q_full);
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_base + i * kKeys;
         const uint32_t o_tmem = tmem + lane_base + 2 * kKeys + i * D;
-        float m = -INFINITY, l = 0.0f, corr = 0.0f;
+        float m = -INFINITY, l = 0.0f;  // the row's reference and its sum of 2^(x - m + kUp)
+        int oe = 0;                     // O is in units of 2^oe
         bool dead = false;
         for (int j = 0; j < steps; j++) {
-            const int slot = j % kScaleSlots;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar->sc_full[slot], (j / kScaleSlots) & 1, abort, p.err, limit) &&
-                                             mbar_wait(&bar->s_full[i], j & 1, abort, p.err, limit))) {
+            const int slot = j % kInfoSlots;
+            if (!warp_wait(&bar->info_full[slot], (j / kInfoSlots) & 1, abort, p.err, limit) ||
+                !warp_wait(&bar->s_full[i], j & 1, abort, p.err, limit)) {
                 dead = true;
                 break;
             }
             tc_fence_after();
-            const float *sc = scales + slot * 4 * kKeys;
-            const int there = bar->there[slot], t0 = j * kKeys;
+            const StepInfo &info = bar->info[slot];
+            const int there = info.there, t0 = j * kKeys;
+            const float f0 = row_scale * info.key_scale[0], f1 = row_scale * info.key_scale[1];
             const int seen = min(max(last - t0 + 1, 0), kKeys);
             const bool whole = there == 3 && t0 + kKeys - 1 <= last_min;
-            uint32_t pk[64];
-            float sum, cs;
-            bool fresh = j == 0;
-            for (;;) {
-                if (fresh) {
-                    // set the reference to the row's maximum so far and bring the sums to it
-                    const float mx = fmaxf(m, step_max(s_tmem, sc, qsum, seen, there));
-                    const float f = m == -INFINITY ? 0.0f : exp2_fast(m - mx);
-                    m = mx;
-                    l *= f;
-                    corr *= f;
-                    if (j > 0) {  // the products up to step j - 1 are complete: S of step j was issued after them
+            const int ve = info.value_exp;
+            const float mx = whole ? step_max<false>(s_tmem, f0, f1, seen, there) : step_max<true>(s_tmem, f0, f1, seen, there);
+            // The row's reference follows its maximum only when that has grown by 2^5 (p stays below 2^15):
+            // most steps rescale nothing.
+            if (__any_sync(0xFFFFFFFFu, mx > m + 5.0f) || ve != oe) {
+                const float mn = fmaxf(m, mx);
+                const float lf = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
+                const float f = lf * pow2(oe - ve);
+                m = mn;
+                l *= lf;
+                oe = ve;
+                if (j > 0) {  // the products up to step j - 1 are complete: S of step j was issued after them
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(o_tmem + c0, o);
-                            tmem_ld_wait();
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_tmem + c0, o);
+                        tmem_ld_wait32(o);
 #pragma unroll
-                            for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st32(o_tmem + c0, o);
-                        }
-                        tmem_st_wait();
+                        for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        tmem_st32(o_tmem + c0, o);
                     }
                 }
-                const float ref = m == -INFINITY ? 0.0f : m;
-                if (whole) step_probs<false>(s_tmem, sc, qsum, ref, seen, there, pk, sum, cs);
-                else step_probs<true>(s_tmem, sc, qsum, ref, seen, there, pk, sum, cs);
-                // The reference may lag behind the maximum: only a step whose probabilities add up to more
-                // than 2^16 moves it, and is then taken again; so does the first step in which a row sees
-                // anything (the pages before may be missing).
-                if (fresh || !__any_sync(0xFFFFFFFFu, sum > 65536.0f || (m == -INFINITY && seen > 0))) break;
-                fresh = true;
             }
-            l += sum;
-            corr += cs;
-            {
-                uint32_t half[32];
+            const float ref = m == -INFINITY ? 0.0f : m - kUp;
+            l += whole ? step_probs<false>(s_tmem, f0, f1, ref, seen, there) : step_probs<true>(s_tmem, f0, f1, ref, seen, there);
+            if ((info.bad[0] | info.bad[1] | info.bad[2] | info.bad[3]) != 0) {
+                // a value of NaN is zero in the operand: the rows that see it get their NaN here
 #pragma unroll
-                for (int k = 0; k < 32; k++) half[k] = pk[k];
-                tmem_st32(s_tmem, half);
-#pragma unroll
-                for (int k = 0; k < 32; k++) half[k] = pk[32 + k];
-                tmem_st32(s_tmem + 32, half);
+                for (int k = 0; k < 4; k++) {
+                    const int n = seen - 32 * k;
+                    const uint32_t mine = n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
+                    if (info.bad[k] & mine) l = __int_as_float(0x7FFFFFFF);
+                }
             }
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&bar->p_full[i]);
+            warp_arrive(&bar->p_full[i]);
         }
         if (!dead && steps > 0)
-            dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&bar->o_full[i], 0, abort, p.err, limit));
+            dead = !warp_wait(&bar->o_full[i], 0, abort, p.err, limit);
         if (!dead) {
             tc_fence_after();
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float inv = l == 0.0f ? 0.0f : pow2(oe - (int)kUp) / (l * pow2(-(int)kUp));
             uint16_t *dst = p.out + (long long)(w.first + rw / p.g) * p.out_stride + (long long)(h * p.g + rw % p.g) * D;
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
                 if (steps > 0) {
                     tmem_ld32(o_tmem + c0, o);
-                    tmem_ld_wait();
+                    tmem_ld_wait32(o);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; k++) o[k] = 0;
@@ -375,196 +504,225 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                         uint32_t u[4];
 #pragma unroll
                         for (int e = 0; e < 4; e++)
-                            u[e] = pack_bf16((__uint_as_float(o[k + 2 * e]) + corr) * inv,
-                                             (__uint_as_float(o[k + 2 * e + 1]) + corr) * inv);
+                            u[e] = pack_bf16(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
                         *reinterpret_cast<uint4 *>(dst + c0 + k) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
             }
         }
     } else if (warp < 10) {
-        // ---------------- keys: two tokens per thread ----------------
-        const int th = threadIdx.x - 256;  // 0 .. 63: token th of the step's first and second page
+        // ---------------- keys: a warp per page, two tokens per thread ----------------
+        const int k = warp - 8;
         for (int j = 0; j < steps; j++) {
-            const int slot = j % kScaleSlots, s = j & 1;
-            uint4 u[2][D / 32];
-            uint32_t sm[2];
-            int there = 0;
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const int t0 = j * kKeys + k * SHERRY_KV4_PAGE;
-                int page = -1;
-                if (t0 < keys) {
-                    page = t0 / SHERRY_KV4_PAGE < p.c.width ? __ldg(p.c.table + (long long)w.b * p.c.table_stride + t0 / SHERRY_KV4_PAGE) : -1;
-                    if (page < 0 || page >= p.c.pages) {
-                        page = -1;
-                        if (th == 0) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
-                    }
-                }
-                sm[k] = 0;
-#pragma unroll
-                for (int e = 0; e < D / 32; e++) u[k][e] = make_uint4(0, 0, 0, 0);
-                if (page >= 0) {
-                    there |= 1 << k;
-                    const uint8_t *blk = kv4_block<D>(p.c, page, h, 0);
-                    const uint4 *src = reinterpret_cast<const uint4 *>(blk + th * Kv4<D>::kRow);
-#pragma unroll
-                    for (int e = 0; e < D / 32; e++) u[k][e] = __ldg(src + e);
-                    sm[k] = __ldg(reinterpret_cast<const uint32_t *>(blk + Kv4<D>::kCodes) + th);
-                }
-            }
+            const int slot = j % kInfoSlots, s = j & 1;
+            if (!warp_wait(&bar->raw_full[s], (j >> 1) & 1, abort, p.err, limit)) break;
+            const uint8_t *blk = raw + (2 * s + k) * T::kPage;
+            const int there = bar->there[s];
+            // tokens past the sequence's end may hold anything: they count as zeros
+            const int in = there >> k & 1 ? w.len - j * kKeys - k * SHERRY_KV4_PAGE : 0;
+            const uint32_t *pairs = reinterpret_cast<const uint32_t *>(blk + Kv4<D>::kCodes);
+            const uint32_t sm[2] = {lane < in ? pairs[lane] : 0u, lane + 32 < in ? pairs[lane + 32] : 0u};
+            const int e = exp_for(warp_max(fmaxf(pair_most(sm[0]), pair_most(sm[1]))), -7);
             // The slot is free: k_empty of step j - 3 was waited for, and its products were issued after
             // the softmax of step j - 4 was done.
-            float *sc = scales + slot * 4 * kKeys;
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const float st = kv4_step(sm[k]);
-                sc[64 * k + th] = st * p.scale2;
-                sc[kKeys + 64 * k + th] = (kv4_low(sm[k]) + 8.0f * st) * p.scale2;
+            if (lane == 0) {
+                bar->info[slot].key_scale[k] = pow2(e);
+                if (k == 0) bar->info[slot].there = there;
             }
-            if (th == 0) bar->there[slot] = there;
-            mbar_arrive(&bar->sc_full[slot]);
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar->k_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit))) break;
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const int t = 64 * k + th;
-                uint8_t *dst = sk + s * T::kOp + t * 128;
-#pragma unroll
-                for (int e = 0; e < D / 32; e++) {
-                    const uint32_t x[4] = {u[k][e].x, u[k][e].y, u[k][e].z, u[k][e].w};
+            warp_arrive(&bar->info_full[slot]);
+            if (!warp_wait(&bar->k_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
+            const float down = pow2(-e);
+#pragma unroll 1
+            for (int t = 0; t < 2; t++) {
+                const int row = lane + 32 * t, tok = SHERRY_KV4_PAGE * k + row;
+                const float st = kv4_step(sm[t]) * down, lo = kv4_low(sm[t]) * down;
+                const uint32_t s0 = pack_f16(st * 16777216.0f, st * 16777216.0f), s1 = pack_f16(st * 1048576.0f, st * 1048576.0f);
+                const uint32_t m2 = pack_f16(lo, lo);
+                const uint8_t *src = blk + row * Kv4<D>::kRow;
+                uint8_t *dst = sk + s * T::kOp + tok * 128;
+#pragma unroll 2
+                for (int q = 0; q < D / 32; q++) {
+                    // 16-byte pieces of a row in an order that keeps eight rows out of each other's banks
+                    const int qq = (q + (D == 128 ? row >> 1 : row >> 2)) & (D / 32 - 1);
+                    uint4 u = *reinterpret_cast<const uint4 *>(src + 16 * qq);
+                    if (row >= in) u = make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                    uint8_t *half = dst + (qq / 2) * (kKeys * 128);
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        const int c = 4 * e + i;  // 8-element chunk of the row
-                        *reinterpret_cast<uint4 *>(dst + (c / 8) * (kKeys * 128) + (((c & 7) ^ (t & 7)) << 4)) =
-                            make_uint4(code_pair8(x[i]), code_pair8(x[i] >> 4), code_pair8(x[i] >> 8), code_pair8(x[i] >> 12));
+                        const int c = (4 * qq + i) & 7;  // 8-element chunk of the 128-byte row
+                        const uint32_t y = x[i] >> 8;
+                        *reinterpret_cast<uint4 *>(half + ((c ^ (tok & 7)) << 4)) =
+                            make_uint4(value_pair<0x000F000F>(x[i], s0, m2), value_pair<0x00F000F0>(x[i], s1, m2),
+                                       value_pair<0x000F000F>(y, s0, m2), value_pair<0x00F000F0>(y, s1, m2));
                     }
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bar->k_full[s]);
+            warp_arrive(&bar->k_full[s]);
+            warp_arrive(&bar->raw_empty[s]);
         }
     } else if (warp < 12) {
-        // ---------------- values: eight tokens of D / 32 words per thread, transposed ----------------
-        const int th = threadIdx.x - 320;           // 0 .. 63
-        const int grp = (th & 7) + 8 * (th >> 5);   // tokens 8 grp .. 8 grp + 7 of the step
-        const int qd = (th >> 3) & 3;               // words qd D / 32 ...
-        constexpr int NW = D / 32;
+        // ---------------- values: a warp per page, eight tokens per thread, transposed ----------------
+        const int k = warp - 10;
+        const int grp = lane & 7, qd = lane >> 3;  // tokens 8 grp ... of the page, word qd of each four
+        const int odd = grp & 1;                   // these read the tokens of a pair in the other order, for the banks
+        int ve = -1000;                            // both warps follow the same values' power of two
         for (int j = 0; j < steps; j++) {
-            const int slot = j % kScaleSlots, s = j & 1;
-            uint32_t x[8][NW];
-            uint32_t sm[2] = {0, 0};
+            const int slot = j % kInfoSlots, s = j & 1;
+            if (!warp_wait(&bar->raw_full[s], (j >> 1) & 1, abort, p.err, limit)) break;
+            const int there = bar->there[s];
+            const uint8_t *blk = raw + 2 * s * T::kPage + Kv4<D>::kBlock;  // the first page's values
+            uint32_t all[4];                       // pairs of tokens lane + 32 i of the step
 #pragma unroll
-            for (int t = 0; t < 8; t++)
-#pragma unroll
-                for (int e = 0; e < NW; e++) x[t][e] = 0;
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const int t0 = j * kKeys + k * SHERRY_KV4_PAGE;
-                if (t0 >= keys) continue;
-                const int page = t0 / SHERRY_KV4_PAGE < p.c.width ? __ldg(p.c.table + (long long)w.b * p.c.table_stride + t0 / SHERRY_KV4_PAGE) : -1;
-                if (page < 0 || page >= p.c.pages) continue;
-                const uint8_t *blk = kv4_block<D>(p.c, page, h, 1);
-                sm[k] = __ldg(reinterpret_cast<const uint32_t *>(blk + Kv4<D>::kCodes) + th);
-                if (grp / 8 == k) {
-                    const uint8_t *src = blk + (grp & 7) * 8 * Kv4<D>::kRow + qd * NW * 4;
-#pragma unroll
-                    for (int t = 0; t < 8; t++) {
-                        if (NW == 4) {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + t * Kv4<D>::kRow));
-                            x[t][0] = v.x, x[t][1] = v.y, x[t][NW - 2] = v.z, x[t][NW - 1] = v.w;
-                        } else {
-                            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + t * Kv4<D>::kRow));
-                            x[t][0] = v.x, x[t][1] = v.y;
-                        }
-                    }
-                }
+            for (int i = 0; i < 4; i++) {
+                const bool in = (there >> (i / 2) & 1) && j * kKeys + lane + 32 * i < w.len;
+                all[i] = in ? reinterpret_cast<const uint32_t *>(blk + (i / 2) * T::kPage + Kv4<D>::kCodes)[lane + 32 * (i & 1)] : 0u;
             }
+            const float most = warp_max(fmaxf(fmaxf(pair_most(all[0]), pair_most(all[1])), fmaxf(pair_most(all[2]), pair_most(all[3]))));
+            // 2^-8 when it is set; it follows when values reach 2^-6
+            if (exp_for(most, -7) > ve) ve = exp_for(most, -8);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pair_bad(all[i]));
+                if (k == 0 && lane == 0) bar->info[slot].bad[i] = bad;
+            }
+            if (k == 0 && lane == 0) bar->info[slot].value_exp = ve;
             // free as the keys' part is: v_empty of step j - 3 was waited for
-            float *sc = scales + slot * 4 * kKeys + 2 * kKeys;
+            warp_arrive(&bar->info_full[slot]);
+            blk += k * T::kPage;
+            const int in = there >> k & 1 ? w.len - j * kKeys - k * SHERRY_KV4_PAGE - 8 * grp : 0;  // tokens of the eight that are there
+            const float down = pow2(-ve);
+            uint32_t s0[4], s1[4], m2[4];
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const float st = kv4_step(sm[k]);
-                sc[64 * k + th] = st;
-                sc[kKeys + 64 * k + th] = kv4_low(sm[k]) + 8.0f * st;
+            for (int t = 0; t < 4; t++) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(blk + Kv4<D>::kCodes + 4 * (8 * grp + 2 * t));
+                const uint32_t a = 2 * t < in && !pair_bad(u.x) ? u.x : 0u, b = 2 * t + 1 < in && !pair_bad(u.y) ? u.y : 0u;
+                const float sa = kv4_step(a) * down, sb = kv4_step(b) * down;
+                s0[t] = pack_f16(sa * 16777216.0f, sb * 16777216.0f);
+                s1[t] = pack_f16(sa * 1048576.0f, sb * 1048576.0f);
+                m2[t] = pack_f16(kv4_low(a) * down, kv4_low(b) * down);
             }
-            mbar_arrive(&bar->sc_full[slot]);
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar->v_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit))) break;
-            uint8_t *dst = sv + s * T::kOp + (grp / 8) * (D * 128);
-#pragma unroll
-            for (int e = 0; e < NW; e++) {
-                const int d0 = 8 * (qd * NW + e);
+            if (!warp_wait(&bar->v_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
+            const uint32_t sel_lo = odd ? 0x1054u : 0x5410u, sel_hi = odd ? 0x3276u : 0x7632u;
+            uint8_t *dst = sv + s * T::kOp + k * (D * 128);
+            const uint8_t *src = blk + 8 * grp * Kv4<D>::kRow;
+#pragma unroll 1
+            for (int e = 0; e < D / 32; e++) {
+                const int word = 4 * ((e + (grp >> 1)) & (D / 32 - 1)) + qd;
                 uint32_t lo[4], hi[4];
 #pragma unroll
                 for (int t = 0; t < 4; t++) {
-                    lo[t] = prmt(x[2 * t][e], x[2 * t + 1][e], 0x5410);
-                    hi[t] = prmt(x[2 * t][e], x[2 * t + 1][e], 0x7632);
+                    const uint32_t a = *reinterpret_cast<const uint32_t *>(src + (2 * t + odd) * Kv4<D>::kRow + 4 * word);
+                    const uint32_t b = *reinterpret_cast<const uint32_t *>(src + (2 * t + 1 - odd) * Kv4<D>::kRow + 4 * word);
+                    lo[t] = prmt(a, b, sel_lo);
+                    hi[t] = prmt(a, b, sel_hi);
                 }
+                uint8_t *row = dst + 8 * word * 128;
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const uint32_t *y = i < 4 ? lo : hi;
-                    const int d = d0 + i;
-                    *reinterpret_cast<uint4 *>(dst + d * 128 + (((grp & 7) ^ (d & 7)) << 4)) =
-                        make_uint4(code_pair8(y[0] >> (4 * (i & 3))), code_pair8(y[1] >> (4 * (i & 3))),
-                                   code_pair8(y[2] >> (4 * (i & 3))), code_pair8(y[3] >> (4 * (i & 3))));
+                for (int i = 0; i < 8; i += 2) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int t = 0; t < 4; t++) y[t] = (i < 4 ? lo[t] : hi[t]) >> (4 * (i & 2));
+                    *reinterpret_cast<uint4 *>(row + i * 128 + ((grp ^ i) << 4)) =
+                        make_uint4(value_pair<0x000F000F>(y[0], s0[0], m2[0]), value_pair<0x000F000F>(y[1], s0[1], m2[1]),
+                                   value_pair<0x000F000F>(y[2], s0[2], m2[2]), value_pair<0x000F000F>(y[3], s0[3], m2[3]));
+                    *reinterpret_cast<uint4 *>(row + (i + 1) * 128 + ((grp ^ (i + 1)) << 4)) =
+                        make_uint4(value_pair<0x00F000F0>(y[0], s1[0], m2[0]), value_pair<0x00F000F0>(y[1], s1[1], m2[1]),
+                                   value_pair<0x00F000F0>(y[2], s1[2], m2[2]), value_pair<0x00F000F0>(y[3], s1[3], m2[3]));
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bar->v_full[s]);
+            warp_arrive(&bar->v_full[s]);
+            warp_arrive(&bar->raw_empty[s]);
         }
-    } else if (lane == 0 && steps > 0) {
-        // ---------------- products ----------------
-        bool ok = mbar_wait(&bar->q_full, 0, abort, p.err, limit);
-        bool issued = false;
-        const uint32_t q_addr = smem_u32(sq), k_addr = smem_u32(sk), v_addr = smem_u32(sv);
-        auto scores = [&](int i, int s) {  // S_i = Q_i K^T
-            tc_fence_after();
+    } else if (warp == 13) {
+        // ---------------- pages ----------------
+        if (lane == 0) {
+            int it = 0;
+            for (; it < steps; it++) {
+                const int s = it & 1;
+                int page[2], there = 0;
 #pragma unroll
-            for (int k = 0; k < D / 16; k++) {
-                const uint32_t off = (k / 4) * (128 * 128) + (k & 3) * 32;
-                umma_f16(tmem + i * kKeys, smem_desc_sw128(q_addr + i * T::kQ + off),
-                         smem_desc_sw128(k_addr + s * T::kOp + off), kIdescBf16<kKeys>, k != 0);
-            }
-            issued = true;
-            umma_commit(&bar->s_full[i]);
-        };
-        if (ok) ok = mbar_wait(&bar->k_full[0], 0, abort, p.err, limit);
-        if (ok) {
-            scores(0, 0);
-            scores(1, 0);
-            umma_commit(&bar->k_empty[0]);
-        }
-        for (int j = 0; ok && j < steps; j++) {
-            const int s = j & 1, ph = (j >> 1) & 1;
-            ok = mbar_wait(&bar->v_full[s], ph, abort, p.err, limit);
-            for (int i = 0; ok && i < 2; i++) {
-                ok = mbar_wait(&bar->p_full[i], j & 1, abort, p.err, limit);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; k++)
-                    umma_f16_tmem_a(tmem + 2 * kKeys + i * D, tmem + i * kKeys + 8 * k,
-                                    smem_desc_sw128(v_addr + s * T::kOp + (k / 4) * (D * 128) + (k & 3) * 32), kIdescBf16<D>,
-                                    j != 0 || k != 0);
-                if (j + 1 < steps) {
-                    if (i == 0) {
-                        ok = mbar_wait(&bar->k_full[s ^ 1], ((j + 1) >> 1) & 1, abort, p.err, limit);
-                        if (!ok) break;
-                    }
-                    scores(i, s ^ 1);
-                } else {
-                    umma_commit(&bar->o_full[i]);
+                for (int k = 0; k < 2; k++) {
+                    const int t0 = it * kKeys + k * SHERRY_KV4_PAGE;
+                    page[k] = t0 < keys ? __ldg(p.c.table + (long long)w.b * p.c.table_stride + t0 / SHERRY_KV4_PAGE) : -1;
+                    if (page[k] >= 0 && page[k] < p.c.pages) there |= 1 << k;
+                    else if (t0 < keys) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
                 }
+                if (!mbar_wait(&bar->raw_empty[s], ((it >> 1) & 1) ^ 1, abort, p.err, limit)) break;
+                bar->there[s] = there;
+                if (there == 0) {
+                    mbar_arrive(&bar->raw_full[s]);
+                    continue;
+                }
+                mbar_arrive_expect_tx(&bar->raw_full[s], (there == 3 ? 2 : 1) * T::kPage);
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+                    if (there >> k & 1)
+                        bulk_load(smem_u32(raw + (2 * s + k) * T::kPage), kv4_block<D>(p.c, page[k], h, 0), T::kPage, &bar->raw_full[s]);
             }
-            if (ok) {
-                umma_commit(&bar->v_empty[s]);
-                if (j + 1 < steps) umma_commit(&bar->k_empty[s ^ 1]);
-            }
-        }
-        // every issued product is done before tensor and shared memory are released
-        if (issued) {
-            umma_commit(&bar->drain);
+            // every copy lands before shared memory is released
             volatile int no_abort = 0;
-            mbar_wait(&bar->drain, 0, &no_abort, p.err, kDrainLimit);
+            for (int j = it < 2 ? 0 : it - 2; j < it; j++) mbar_wait(&bar->raw_full[j & 1], (j >> 1) & 1, &no_abort, p.err, kDrainLimit);
+        }
+    } else {
+        if (steps > 0) {
+            // ---------------- products ----------------
+            // The whole warp walks and waits, one elected lane issues.
+            const uint32_t q_lo = (smem_u32(sq) >> 4) | (1u << 16), k_lo = (smem_u32(sk) >> 4) | (1u << 16),
+                           v_lo = (smem_u32(sv) >> 4) | (1u << 16);
+            auto scores = [&](int i, int s) {  // S_i = Q_i K^T
+                tc_fence_after();
+                if (elect_one()) {
+mma_ss_all<0, D / 16, 128>(tmem + i * kKeys, q_lo + i * (T::kQ >> 4), k_lo + s * (T::kOp >> 4), kIdesc<kKeys>);
+                    umma_commit(&bar->s_full[i]);
+                }
+                __syncwarp();
+            };
+            bool ok = warp_wait(&bar->q_full, 0, abort, p.err, limit) && warp_wait(&bar->k_full[0], 0, abort, p.err, limit);
+            const bool issued = ok;
+            if (ok) {
+                scores(0, 0);
+                scores(1, 0);
+                if (elect_one()) umma_commit(&bar->k_empty[0]);
+            }
+            for (int j = 0; ok && j < steps; j++) {
+                const int s = j & 1, ph = (j >> 1) & 1;
+                ok = warp_wait(&bar->v_full[s], ph, abort, p.err, limit);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    if (!ok) break;
+                    ok = warp_wait(&bar->p_full[i], j & 1, abort, p.err, limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect_one()) {
+mma_ts_all<0, kKeys / 16, D>(tmem + 2 * kKeys + i * D, tmem + i * kKeys, v_lo + s * (T::kOp >> 4),
+                                                     kIdesc<D>, j != 0);
+                        if (j + 1 == steps) umma_commit(&bar->o_full[i]);
+                    }
+                    __syncwarp();
+                    if (j + 1 < steps) {
+                        if (i == 0) {
+                            ok = warp_wait(&bar->k_full[s ^ 1], ((j + 1) >> 1) & 1, abort, p.err, limit);
+                            if (!ok) break;
+                        }
+                        scores(i, s ^ 1);
+                    }
+                }
+                if (ok && elect_one()) {
+                    umma_commit(&bar->v_empty[s]);
+                    if (j + 1 < steps) umma_commit(&bar->k_empty[s ^ 1]);
+                }
+                __syncwarp();
+            }
+            // every issued product is done before tensor and shared memory are released
+            if (issued) {
+                if (elect_one()) umma_commit(&bar->drain);
+                __syncwarp();
+                volatile int no_abort = 0;
+                mbar_wait(&bar->drain, 0, &no_abort, p.err, kDrainLimit);
+            }
         }
     }
     tc_fence_before();

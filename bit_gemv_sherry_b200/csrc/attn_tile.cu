@@ -37,7 +37,9 @@ namespace {
 constexpr int kRowsTile = 128;
 constexpr int kRowsCta = 2 * kRowsTile;
 constexpr int kKeys = 128;                 // tokens per step: two pages
-constexpr int kTileThreads = 14 * 32;
+// Four warpgroups launched with 128 registers a thread (the last: issue, copies and two idle warps);
+// the softmax takes 176, the decoders 96, the last 64: 2 * 176 + 96 + 64 = 4 * 128.
+constexpr int kTileThreads = 16 * 32;
 constexpr int kInfoSlots = 4;
 constexpr float kUp = 10.0f;               // a probability of 1 is held as 2^10
 constexpr int kAllSeen = 0x7FFFFFFF - 2 * kKeys;
@@ -95,11 +97,21 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ f2 add2(f2 a, f2 b) {
     f2 d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // tmem_ld_wait that the loaded registers depend on: nothing that reads them moves above it.
 __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
@@ -264,68 +276,105 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-// Largest score of the row in this step (-inf if none is seen); f0, f1 >= 0 scale the pages' scores.
-// MASK: the row sees the step's first `seen` tokens, of pages that are there.
-template <bool MASK>
-__device__ __forceinline__ float step_max(uint32_t s_tmem, float f0, float f1, int seen, int there) {
-    float page[2];
+// A row's reference m of the exponentials and, in two halves, its sum of 2^(x - m + kUp).
+struct RowSums {
+    float m;
+    f2 l;
+};
+
+// Moves the reference of the rows that need it (the largest score of this part of the step is not
+// below it by kUp still, or nothing was seen before) and brings all that was computed against the
+// old one to the new one: the sum, the step's probabilities stored so far and, past the first step, O.
+// r: the part's scores, n: tokens of it that the row sees.
+template <int D>
+__device__ __forceinline__ void move_reference(uint32_t s_tmem, uint32_t o_tmem, int c0, uint32_t (&r)[32], float f, int n, bool first,
+                                               RowSums &row) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 32; i++) mx = fmaxf(mx, i < n ? __uint_as_float(r[i]) : -INFINITY);
+    mx = mx == -INFINITY ? mx : f * mx;  // 0 * -inf would be NaN
+    const float up = fmaxf(row.m, mx);
+    const float by = row.m == -INFINITY ? 0.0f : exp2_fast(row.m - up);
+    row.m = up;
+    row.l = mul2(row.l, pair2(by, by));
+    const uint32_t by2 = pack_f16(by, by);
 #pragma unroll 1
-    for (int c0 = 0; c0 < kKeys; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(s_tmem + c0, r);
-        tmem_ld_wait32(r);
-        const int n = MASK ? (there >> (c0 / SHERRY_KV4_PAGE) & 1 ? seen - c0 : 0) : 32;
-        float m[4];
+    for (int c = 0; c < c0; c += 32) {  // probabilities of parts before this one
+        uint32_t q[16];
+        tmem_ld16(s_tmem + c / 2, q);
+        tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 4; k++) m[k] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 32; i++) {
-            const float v = __uint_as_float(r[i]);
-            m[i & 3] = fmaxf(m[i & 3], !MASK || i < n ? v : -INFINITY);
-        }
-        const float v = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-        if (c0 == 0) page[0] = v;
-        else if (c0 == 32) page[0] = fmaxf(page[0], v);
-        else if (c0 == 64) page[1] = v;
-        else page[1] = fmaxf(page[1], v);
+        for (int k = 0; k < 16; k++) asm volatile("mul.rn.f16x2 %0, %0, %1;" : "+r"(q[k]) : "r"(by2));
+        tmem_st16(s_tmem + c / 2, q);
     }
-    // 0 * -inf would be NaN
-    const float a = page[0] == -INFINITY ? page[0] : f0 * page[0], b = page[1] == -INFINITY ? page[1] : f1 * page[1];
-    return fmaxf(a, b);
+    if (!first) {
+        // the products up to the step before are complete: this step's S was issued after them
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            tmem_ld32(o_tmem + c, r);
+            tmem_ld_wait32(r);
+#pragma unroll
+            for (int k = 0; k < 32; k++) r[k] = __float_as_uint(__uint_as_float(r[k]) * by);
+            tmem_st32(o_tmem + c, r);
+        }
+    }
+    tmem_st_wait();
+    tmem_ld32(s_tmem + c0, r);  // this part's columns are not written yet
+    tmem_ld_wait32(r);
 }
 
-// P = 2^(f S - ref) of the step as fp16 into the tensor memory of S (the columns that are read
-// already), and their sum.
-template <bool MASK>
-__device__ __forceinline__ float step_probs(uint32_t s_tmem, float f0, float f1, float ref, int seen, int there) {
-    const f2 nm = pair2(-ref, -ref);
-    f2 sum2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
+// P = 2^(f S - m + kUp) of the step as fp16 into the tensor memory of S (columns that are read already).
+// f0, f1 >= 0 scale the pages' scores.  MASK: the row sees the step's first `seen` tokens, of pages that
+// are there.  The reference lags behind the row's maximum: it moves only when 32 probabilities add up
+// to more than fp16 holds, or when a row sees its first token.
+template <int D, bool MASK>
+__device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, float f0, float f1, int seen, int there, bool first,
+                                           RowSums &row) {
+    uint32_t buf[2][32];
+    tmem_ld32(s_tmem, buf[0]);
 #pragma unroll 1
-    for (int c0 = 0; c0 < kKeys; c0 += 32) {
-        uint32_t r[32], pk[16];
-        tmem_ld32(s_tmem + c0, r);
-        tmem_ld_wait32(r);
-        const float fp = c0 < SHERRY_KV4_PAGE ? f0 : f1;
+    for (int page = 0; page < 2; page++) {
+        const float fp = page ? f1 : f0;
         const f2 f = pair2(fp, fp);
-        const int n = MASK ? (there >> (c0 / SHERRY_KV4_PAGE) & 1 ? seen - c0 : 0) : 32;
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            float a, b;
-            split2(fma2(f, pair2u(r[i], r[i + 1]), nm), a, b);
-            a = exp2_fast(a);
-            b = exp2_fast(b);
-            if (MASK) {
-                a = i < n ? a : 0.0f;
-                b = i + 1 < n ? b : 0.0f;
+        for (int half = 0; half < 2; half++) {
+            const int c0 = 64 * page + 32 * half;
+            uint32_t(&r)[32] = buf[half];
+            tmem_ld_wait32(r);
+            if (half == 0) tmem_ld32(s_tmem + c0 + 32, buf[1]);  // behind this part's arithmetic
+            else if (page == 0) tmem_ld32(s_tmem + c0 + 32, buf[0]);
+            const int n = MASK ? (there >> page & 1 ? seen - c0 : 0) : 32;
+            uint32_t pk[16];
+            f2 sum;
+            for (bool moved = false;; moved = true) {
+                const float ref = row.m == -INFINITY ? 0.0f : row.m - kUp;
+                const f2 nm = pair2(-ref, -ref);
+                f2 sum2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    float a, b;
+                    split2(fma2(f, pair2u(r[i], r[i + 1]), nm), a, b);
+                    a = exp2_fast(a);
+                    b = exp2_fast(b);
+                    if (MASK) {
+                        a = i < n ? a : 0.0f;
+                        b = i + 1 < n ? b : 0.0f;
+                    }
+                    sum2[(i / 2) & 1] = add2(sum2[(i / 2) & 1], pair2(a, b));
+                    pk[i / 2] = pack_f16(a, b);
+                }
+                sum = add2(sum2[0], sum2[1]);
+                float a, b;
+                split2(sum, a, b);
+                // once is enough (a row of nothing but NaN has no reference after it either)
+                if (moved || !__any_sync(0xFFFFFFFFu, a + b > 60000.0f || (row.m == -INFINITY && n > 0))) break;
+                tmem_ld_wait32(buf[half ^ 1]);
+                move_reference<D>(s_tmem, o_tmem, c0, r, fp, n, first, row);
             }
-            sum2[(i / 2) & 1] = add2(sum2[(i / 2) & 1], pair2(a, b));
-            pk[i / 2] = pack_f16(a, b);
+            row.l = add2(row.l, sum);
+            tmem_st16(s_tmem + c0 / 2, pk);
         }
-        tmem_st16(s_tmem + c0 / 2, pk);
     }
-    float a, b;
-    split2(add2(sum2[0], sum2[1]), a, b);
-    return a + b;
 }
 
 template <int D>
@@ -383,6 +432,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
 
     if (warp < 8) {
         // ---------------- softmax: a thread owns a row ----------------
+        regs_up<176>();
         const int i = warp >> 2, r = threadIdx.x & 127;      // tile, row of the tile
         const int rw = row0 + i * kRowsTile + r;
         const bool live = rw < nrow;
@@ -428,7 +478,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_base + i * kKeys;
         const uint32_t o_tmem = tmem + lane_base + 2 * kKeys + i * D;
-        float m = -INFINITY, l = 0.0f;  // the row's reference and its sum of 2^(x - m + kUp)
+        RowSums row = {-INFINITY, pair2(0.0f, 0.0f)};
         int oe = 0;                     // O is in units of 2^oe
         bool dead = false;
         for (int j = 0; j < steps; j++) {
@@ -445,17 +495,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             const int seen = min(max(last - t0 + 1, 0), kKeys);
             const bool whole = there == 3 && t0 + kKeys - 1 <= last_min;
             const int ve = info.value_exp;
-            const float mx = whole ? step_max<false>(s_tmem, f0, f1, seen, there) : step_max<true>(s_tmem, f0, f1, seen, there);
-            // The row's reference follows its maximum only when that has grown by 2^5 (p stays below 2^15):
-            // most steps rescale nothing.
-            if (__any_sync(0xFFFFFFFFu, mx > m + 5.0f) || ve != oe) {
-                const float mn = fmaxf(m, mx);
-                const float lf = m == -INFINITY ? 0.0f : exp2_fast(m - mn);
-                const float f = lf * pow2(oe - ve);
-                m = mn;
-                l *= lf;
-                oe = ve;
-                if (j > 0) {  // the products up to step j - 1 are complete: S of step j was issued after them
+            if (ve != oe) {
+                if (j > 0) {
+                    const float f = pow2(oe - ve);
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         uint32_t o[32];
@@ -465,17 +507,19 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                         for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                         tmem_st32(o_tmem + c0, o);
                     }
+                    tmem_st_wait();
                 }
+                oe = ve;
             }
-            const float ref = m == -INFINITY ? 0.0f : m - kUp;
-            l += whole ? step_probs<false>(s_tmem, f0, f1, ref, seen, there) : step_probs<true>(s_tmem, f0, f1, ref, seen, there);
+            if (whole) step_probs<D, false>(s_tmem, o_tmem, f0, f1, seen, there, j == 0, row);
+            else step_probs<D, true>(s_tmem, o_tmem, f0, f1, seen, there, j == 0, row);
             if ((info.bad[0] | info.bad[1] | info.bad[2] | info.bad[3]) != 0) {
                 // a value of NaN is zero in the operand: the rows that see it get their NaN here
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const int n = seen - 32 * k;
                     const uint32_t mine = n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
-                    if (info.bad[k] & mine) l = __int_as_float(0x7FFFFFFF);
+                    if (info.bad[k] & mine) row.l = pair2(__int_as_float(0x7FFFFFFF), 0.0f);
                 }
             }
             tmem_st_wait();
@@ -486,6 +530,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             dead = !warp_wait(&bar->o_full[i], 0, abort, p.err, limit);
         if (!dead) {
             tc_fence_after();
+            float l, l1;
+            split2(row.l, l, l1);
+            l += l1;
             const float inv = l == 0.0f ? 0.0f : pow2(oe - (int)kUp) / (l * pow2(-(int)kUp));
             uint16_t *dst = p.out + (long long)(w.first + rw / p.g) * p.out_stride + (long long)(h * p.g + rw % p.g) * D;
 #pragma unroll 1
@@ -510,7 +557,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                 }
             }
         }
-    } else if (warp < 10) {
+    } else if (warp < 12) {
+        regs_down<96>();
+        if (warp < 10) {
         // ---------------- keys: a warp per page, two tokens per thread ----------------
         const int k = warp - 8;
         for (int j = 0; j < steps; j++) {
@@ -562,7 +611,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             warp_arrive(&bar->k_full[s]);
             warp_arrive(&bar->raw_empty[s]);
         }
-    } else if (warp < 12) {
+        } else {
         // ---------------- values: a warp per page, eight tokens per thread, transposed ----------------
         const int k = warp - 10;
         const int grp = lane & 7, qd = lane >> 3;  // tokens 8 grp ... of the page, word qd of each four
@@ -636,7 +685,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             warp_arrive(&bar->v_full[s]);
             warp_arrive(&bar->raw_empty[s]);
         }
-    } else if (warp == 13) {
+        }
+    } else {
+        regs_down<64>();
+        if (warp == 13) {
         // ---------------- pages ----------------
         if (lane == 0) {
             int it = 0;
@@ -666,8 +718,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             volatile int no_abort = 0;
             for (int j = it < 2 ? 0 : it - 2; j < it; j++) mbar_wait(&bar->raw_full[j & 1], (j >> 1) & 1, &no_abort, p.err, kDrainLimit);
         }
-    } else {
-        if (steps > 0) {
+        } else if (warp == 12 && steps > 0) {
             // ---------------- products ----------------
             // The whole warp walks and waits, one elected lane issues.
             const uint32_t q_lo = (smem_u32(sq) >> 4) | (1u << 16), k_lo = (smem_u32(sk) >> 4) | (1u << 16),

@@ -41,7 +41,7 @@ constexpr int kKeys = 128;                 // tokens per step: two pages
 // the softmax takes 176, the decoders 96, the last 64: 2 * 176 + 96 + 64 = 4 * 128.
 constexpr int kTileThreads = 16 * 32;
 constexpr int kInfoSlots = 4;
-constexpr float kUp = 8.0f;                // a probability of 1 is held as 2^8: 128 of them add up below fp16's largest
+constexpr float kUp = 10.0f;               // a probability of 1 is held as 2^10
 constexpr int kAllSeen = 0x7FFFFFFF - 2 * kKeys;
 constexpr int kTmemCols = 512;             // S0, S1 (128 columns each), O0, O1 (D each)
 constexpr long long kDrainLimit = 1000000000LL;
@@ -323,49 +323,11 @@ __device__ __forceinline__ void move_reference(uint32_t s_tmem, uint32_t o_tmem,
     tmem_ld_wait32(r);
 }
 
-// P = 2^(f S - m + kUp) of the step as fp16 into the tensor memory of S; f0, f1 >= 0 scale the pages'
-// scores.  The reference lags behind the row's maximum: it moves only when probabilities add up to more
-// than fp16 holds, or when a row sees its first token.
-//
-// The usual step: every row sees all of it and has a reference, and nothing overflows (false otherwise, S
-// as it was).  Without a branch between the parts a warp has enough independent work to keep the
-// exponentials busy alone: 32 at a time with a test after each took 2,340 clocks a step.
-__device__ __forceinline__ bool step_fast(uint32_t s_tmem, float f0, float f1, RowSums &row) {
-    const f2 nm = pair2(kUp - row.m, kUp - row.m);
-    f2 sum2[4];
-#pragma unroll
-    for (int k = 0; k < 4; k++) sum2[k] = pair2(0.0f, 0.0f);
-    uint32_t buf[2][32], pk[2][32];
-    tmem_ld32(s_tmem, buf[0]);
-#pragma unroll
-    for (int c = 0; c < 4; c++) {
-        uint32_t(&r)[32] = buf[c & 1];
-        tmem_ld_wait32(r);
-        if (c < 3) tmem_ld32(s_tmem + 32 * c + 32, buf[(c + 1) & 1]);  // behind this part's arithmetic
-        const f2 f = c < 2 ? pair2(f0, f0) : pair2(f1, f1);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            float a, b;
-            split2(fma2(f, pair2u(r[i], r[i + 1]), nm), a, b);
-            a = exp2_fast(a);
-            b = exp2_fast(b);
-            sum2[(i / 2) & 3] = add2(sum2[(i / 2) & 3], pair2(a, b));
-            pk[c / 2][(c & 1) * 16 + i / 2] = pack_f16(a, b);
-        }
-    }
-    const f2 sum = add2(add2(sum2[0], sum2[1]), add2(sum2[2], sum2[3]));
-    float a, b;
-    split2(sum, a, b);
-    if (__any_sync(0xFFFFFFFFu, a + b > 60000.0f)) return false;
-    row.l = add2(row.l, sum);
-    tmem_st32(s_tmem, pk[0]);
-    tmem_st32(s_tmem + 32, pk[1]);
-    return true;
-}
-
-// Any step: the row sees its first `seen` tokens, of pages that are there.  Columns are written when they
-// have been read.
-template <int D>
+// P = 2^(f S - m + kUp) of the step as fp16 into the tensor memory of S (columns that are read already).
+// f0, f1 >= 0 scale the pages' scores.  MASK: the row sees the step's first `seen` tokens, of pages that
+// are there.  The reference lags behind the row's maximum: it moves only when 32 probabilities add up
+// to more than fp16 holds, or when a row sees its first token.
+template <int D, bool MASK>
 __device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, float f0, float f1, int seen, int there, bool first,
                                            RowSums &row) {
     uint32_t buf[2][32];
@@ -381,7 +343,7 @@ __device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, flo
             tmem_ld_wait32(r);
             if (half == 0) tmem_ld32(s_tmem + c0 + 32, buf[1]);  // behind this part's arithmetic
             else if (page == 0) tmem_ld32(s_tmem + c0 + 32, buf[0]);
-            const int n = there >> page & 1 ? seen - c0 : 0;
+            const int n = MASK ? (there >> page & 1 ? seen - c0 : 0) : 32;
             uint32_t pk[16];
             f2 sum;
             for (bool moved = false;; moved = true) {
@@ -394,8 +356,10 @@ __device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, flo
                     split2(fma2(f, pair2u(r[i], r[i + 1]), nm), a, b);
                     a = exp2_fast(a);
                     b = exp2_fast(b);
-                    a = i < n ? a : 0.0f;
-                    b = i + 1 < n ? b : 0.0f;
+                    if (MASK) {
+                        a = i < n ? a : 0.0f;
+                        b = i + 1 < n ? b : 0.0f;
+                    }
                     sum2[(i / 2) & 1] = add2(sum2[(i / 2) & 1], pair2(a, b));
                     pk[i / 2] = pack_f16(a, b);
                 }
@@ -547,8 +511,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                 }
                 oe = ve;
             }
-            if (!whole || __any_sync(0xFFFFFFFFu, row.m == -INFINITY) || !step_fast(s_tmem, f0, f1, row))
-                step_probs<D>(s_tmem, o_tmem, f0, f1, seen, there, j == 0, row);
+            if (whole) step_probs<D, false>(s_tmem, o_tmem, f0, f1, seen, there, j == 0, row);
+            else step_probs<D, true>(s_tmem, o_tmem, f0, f1, seen, there, j == 0, row);
             if ((info.bad[0] | info.bad[1] | info.bad[2] | info.bad[3]) != 0) {
                 // a value of NaN is zero in the operand: the rows that see it get their NaN here
 #pragma unroll

@@ -10,84 +10,101 @@ namespace {
 // ---------------------------------------------------------------------------
 // Few rows: mma.sync on fragments decoded in registers
 // ---------------------------------------------------------------------------
-// The bytes of the cache are the bound: 2 (D / 2 + 4) per token and head.  A unit of work is one
-// page for one key/value head and up to 8 NT rows (query heads that share it, times new tokens).
-// All units of the batch, in the order (sequence, head, row tile, page), are cut into equal runs,
-// one per CTA, so that long and short sequences load every SM alike; a run's pieces that are not
-// whole go to the workspace and a second kernel joins them in the order of the CTAs (no atomics:
-// results do not depend on timing).  One warp copies pages into a ring (a page's keys and values
-// are one contiguous block: one bulk copy); four warps take 16 of a page's tokens each.  The
-// product is S^T = K q^T with 16 tokens by 8 rows: the 8-wide side carries the few rows, so
-// 4 query heads per key/value head fill half of the instruction instead of a quarter.  The 128 of
-// the codes' bf16 is taken out of the first product by starting it at -128 sum(q), and out of the
-// second by -136 times the sum of the rounded p s.
+// The bytes of the cache are the bound: 2 (D / 2 + 4) per token and head.  The work is the pages of the
+// batch in the order (sequence, head, row tile, page), a row tile being up to 8 NT rows (query heads that
+// share a key/value head, times new tokens).  It is cut into equal runs, one per warp, so that long and
+// short sequences load the machine alike; row tiles that a run does not hold whole go to the workspace
+// and a second kernel joins their parts in the order of the runs (no atomics: results do not depend on
+// timing).  A warp works alone: it copies its pages into its own ring (a page's keys and values are one
+// contiguous block: one bulk copy), and no other warp waits for it.
+// The product is S^T = K q^T, 16 tokens by 8 rows: the 8-wide side carries the few rows, so 4 query heads
+// per key/value head fill half of the instruction instead of a quarter.  The 128 of the codes' bf16 is
+// taken out of the first product by starting it at -128 sum(q), and out of the second by -136 times the
+// sum of the rounded p s, which one more product with ones gives.
+// Earlier form: a page shared by four warps, 16 tokens each, filled by a fifth: 1,520 instructions a page
+// of heads of 64 against about 600 here, and 357 us for 32 sequences of 32,768 tokens.
 constexpr int kFewWarps = 4;
-constexpr int kFewThreads = 32 * (kFewWarps + 1);
-constexpr int kFewCtasMax = 1024;  // bounds the workspace
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kFewRunsMax = 2560;  // bounds the workspace
 constexpr int kFewRows = 32;       // rows of a sequence up to which this kernel takes it
+// Starting and ending a row tile costs a warp about as much as this many pages; counted as work where
+// there is enough of it.
+constexpr int kUnitCost = 1;
 
 template <int D, int NT>
 struct Few {
     static constexpr int kRows = 8 * NT;
     static constexpr int kStage = 2 * Kv4<D>::kBlock;
-    static constexpr int kStages = D == 64 ? 8 : 5;
-    static constexpr int kRing = kStages * kStage;
-    static constexpr int kJoin = kRows * D * 4;   // [rows][D] sums of the four warps
-    static constexpr size_t kSmem = kRing + kJoin + 256 * NT + 256;
+    static constexpr int kStages = D == 64 ? 3 : 2;
+    static constexpr int kTiles = 2;  // 16-token tiles whose scores are held at a time
+    static constexpr int kCtas = NT == 1 ? (D == 64 ? 4 : 3) : 2;
+    static constexpr size_t kSmem = kFewWarps * (kStages * (kStage + 16) + 128) + 16;
 };
 
-// Work of a batch: sequence b has `tiles` row tiles of `pages` pages for each head.
+// A sequence's part of the work: `tiles` row tiles of `pages` pages for each head.
 struct SeqWork {
     int first, rows, pages, tiles, len;
 };
 
 template <int ROWS>
 __device__ __forceinline__ SeqWork seq_work(const AttnParams &p, int b) {
-    const Kv4View &c = p.c;
-    const int g = p.g;
     SeqWork s;
     int n;
-    kv4_rows(c, b, s.first, n);
+    kv4_rows(p.c, b, s.first, n);
     s.rows = n;
-    s.len = max(__ldg(c.lens + b), 0);
-    const long long rows = (long long)n * g;
+    s.len = max(__ldg(p.c.lens + b), 0);
+    const long long rows = (long long)n * p.g;
     s.tiles = rows > p.few_rows ? 0 : (int)((rows + ROWS - 1) / ROWS);
     // an empty sequence has one page without keys: its rows are written as zeros
-    s.pages = max((min(s.len, c.width * SHERRY_KV4_PAGE) + SHERRY_KV4_PAGE - 1) / SHERRY_KV4_PAGE, 1);
+    s.pages = max((min(s.len, p.c.width * SHERRY_KV4_PAGE) + SHERRY_KV4_PAGE - 1) / SHERRY_KV4_PAGE, 1);
     return s;
 }
 
-template <int ROWS>
-__device__ __forceinline__ long long seq_units(const AttnParams &p, int b) {
-    if (b >= p.c.B) return 0;
-    const SeqWork s = seq_work<ROWS>(p, b);
-    return (long long)p.c.H * s.tiles * s.pages;
-}
+// The batch's work as this launch divides it.
+struct Work {
+    long long total;  // work of all row tiles: pages, and `cost` for each row tile
+    int cost, runs;
+};
 
-// Sum of the batch's units (every lane of a full warp).
 template <int ROWS>
-__device__ long long all_units(const AttnParams &p) {
-    long long sum = 0;
-    for (int b = threadIdx.x & 31; b < p.c.B; b += 32) sum += seq_units<ROWS>(p, b);
+__device__ Work all_work(const AttnParams &p) {
+    long long pages = 0, units = 0;
+    for (int b = threadIdx.x & 31; b < p.c.B; b += 32) {
+        const SeqWork s = seq_work<ROWS>(p, b);
+        units += (long long)p.c.H * s.tiles;
+        pages += (long long)p.c.H * s.tiles * s.pages;
+    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    return sum;
+    for (int o = 16; o > 0; o >>= 1) {
+        pages += __shfl_xor_sync(0xFFFFFFFFu, pages, o);
+        units += __shfl_xor_sync(0xFFFFFFFFu, units, o);
+    }
+    Work w;
+    w.cost = pages >= 4LL * p.grid ? kUnitCost : 0;
+    w.total = pages + units * w.cost;
+    w.runs = (int)min((long long)p.grid, w.total);
+    return w;
 }
 
-// The sequence that holds unit w (w below all_units) and the units before it.
-template <int ROWS>
-__device__ void find_unit(const AttnParams &p, long long w, int &b, long long &before) {
+// The sequence that holds place x of the work (x below the total), and the work before it; or, with
+// UNITS, the sequence that holds row tile x, and the row tiles before it.
+template <int ROWS, bool UNITS>
+__device__ void find_seq(const AttnParams &p, const Work &w, long long x, int &b, long long &before) {
     const int lane = threadIdx.x & 31;
     long long base = 0;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-        const long long mine = seq_units<ROWS>(p, b0 + lane);
+        long long mine = 0;
+        if (b0 + lane < p.c.B) {
+            const SeqWork s = seq_work<ROWS>(p, b0 + lane);
+            mine = (long long)p.c.H * s.tiles * (UNITS ? 1 : s.pages + w.cost);
+        }
         long long sum = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
             if (lane >= o) sum += v;
         }
-        const unsigned hit = __ballot_sync(0xFFFFFFFFu, base + sum > w);
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, base + sum > x);
         if (hit) {
             const int l = __ffs(hit) - 1;
             b = b0 + l;
@@ -100,40 +117,44 @@ __device__ void find_unit(const AttnParams &p, long long w, int &b, long long &b
     before = base;
 }
 
-// CTA i of n takes units [i W / n, (i + 1) W / n); unit w lies with CTA ((w + 1) n - 1) / W.
-__device__ __forceinline__ long long run_start(long long W, int i, int n) { return W * i / n; }
-__device__ __forceinline__ int run_of(long long W, long long w, int n) { return (int)(((w + 1) * n - 1) / W); }
+// Run i takes places [i T / n, (i + 1) T / n) of the work; place x lies in run ((x + 1) n - 1) / T.
+__device__ __forceinline__ long long run_start(const Work &w, int i) { return w.total * i / w.runs; }
+__device__ __forceinline__ int run_of(const Work &w, long long x) { return (int)(((x + 1) * w.runs - 1) / w.total); }
 
-// A CTA's walk over its run, one piece (part of a (sequence, head, row tile)) at a time.
+// A walk over a run, one piece (pages of one (sequence, head, row tile)) at a time.
 template <int ROWS>
 struct Walk {
-    long long w, end, before;  // position, end of the run, units before sequence b
-    int b;
+    long long x, end, before;  // place, end of the run, work before sequence b
+    int b, cost;
     SeqWork s;
     int h, tile, page0, page1;
 
-    __device__ __forceinline__ void start(const AttnParams &p, long long from, long long to) {
-        w = from;
+    __device__ __forceinline__ void start(const AttnParams &p, const Work &w, long long from, long long to) {
+        x = from;
         end = to;
-        find_unit<ROWS>(p, w, b, before);
+        cost = w.cost;
+        find_seq<ROWS, false>(p, w, x, b, before);
         if (b < p.c.B) s = seq_work<ROWS>(p, b);
     }
     // The next piece: pages [page0, page1) of (b, h, tile); false at the end.
     __device__ __forceinline__ bool next(const AttnParams &p) {
-        if (w >= end) return false;
-        while (w - before >= (long long)p.c.H * s.tiles * s.pages) {
-            before += (long long)p.c.H * s.tiles * s.pages;
-            if (++b >= p.c.B) return false;
-            s = seq_work<ROWS>(p, b);
+        for (;;) {
+            if (x >= end) return false;
+            while (x - before >= (long long)p.c.H * s.tiles * (s.pages + cost)) {
+                before += (long long)p.c.H * s.tiles * (s.pages + cost);
+                if (++b >= p.c.B) return false;
+                s = seq_work<ROWS>(p, b);
+            }
+            const int unit = (int)((x - before) / (s.pages + cost));
+            const long long at = before + (long long)unit * (s.pages + cost);  // the row tile's first place
+            page0 = max((int)(x - at) - cost, 0);
+            page1 = (int)min((long long)s.pages, end - at - cost);
+            h = unit / s.tiles;
+            tile = unit - h * s.tiles;
+            x = at + cost + max(page1, 0);
+            if (page1 > page0) return true;
+            if (page1 <= 0) x = end;  // the run ends before the row tile's first page
         }
-        const long long u = w - before;
-        const int unit = (int)(u / s.pages);
-        page0 = (int)(u - (long long)unit * s.pages);
-        page1 = (int)min((long long)s.pages, page0 + (end - w));
-        h = unit / s.tiles;
-        tile = unit - h * s.tiles;
-        w += page1 - page0;
-        return true;
     }
 };
 
@@ -151,74 +172,71 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return d;
 }
 
-// Barrier of the consumer warps alone.
-__device__ __forceinline__ void few_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory"); }
-
 template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_kernel(const __grid_constant__ AttnParams p) {
     using F = Few<D, NT>;
-    constexpr int kRows = F::kRows, kS = F::kStages, MT = D / 16, WK = D / 32;
+    constexpr int kRows = F::kRows, kS = F::kStages, MT = D / 16, WK = D / 32, kTiles = F::kTiles;
     extern __shared__ __align__(128) uint8_t smem[];
-    float *join = reinterpret_cast<float *>(smem + F::kRing);
-    float *stat = join + kRows * D;                       // [4 warps][rows] maxima, then [rows] sums
-    uint64_t *full = reinterpret_cast<uint64_t *>(stat + 8 * kRows), *empty = full + kS;
-    int *there = reinterpret_cast<int *>(empty + kS);     // per stage: the page exists
-    int *abort = there + kS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kS; s++) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, kFewWarps);
-        }
-        *abort = 0;
+    uint8_t *ring = smem + warp * kS * F::kStage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kFewWarps * kS * F::kStage) + warp * kS;
+    int *there = reinterpret_cast<int *>(smem + kFewWarps * kS * (F::kStage + 8)) + warp * kS;  // the stage's page exists
+    int *abort = reinterpret_cast<int *>(smem + kFewWarps * kS * (F::kStage + 12));
+    // lane 0's walk ahead, for the copies (in shared memory: one lane's few accesses a page)
+    static_assert(sizeof(Walk<kRows>) <= 120, "walk");
+    Walk<kRows> &ahead = *reinterpret_cast<Walk<kRows> *>(smem + kFewWarps * (kS * (F::kStage + 16)) + 16 + 128 * warp);
+    int &ahead_page = *reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(&ahead) + 120);
+    if (lane == 0) {
+        for (int s = 0; s < kS; s++) mbar_init(full + s, 1);
         fence_mbar_init();
     }
+    if (threadIdx.x == 0) *abort = 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");  // lengths and cache come from the kernels before
-    const long long W = all_units<kRows>(p);
-    const int n = (int)min((long long)p.grid, W);
-    if ((int)blockIdx.x >= n) return;
-    const long long from = run_start(W, blockIdx.x, n), to = run_start(W, blockIdx.x + 1, n);
+    const Work work = all_work<kRows>(p);
+    const int run = blockIdx.x + gridDim.x * warp;      // neighbouring runs on different SMs
+    if (run >= work.runs) return;
+    const long long from = run_start(work, run), to = run_start(work, run + 1);
     Walk<kRows> walk;
-    walk.start(p, from, to);
+    walk.start(p, work, from, to);
 
-    if (warp == kFewWarps) {
-        // ---------------- copies ----------------
-        if (lane == 0) {
-            uint32_t it = 0;
-            while (walk.next(p)) {
-                if (walk.s.len > p.c.width * SHERRY_KV4_PAGE) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
-                for (int pg = walk.page0; pg < walk.page1; pg++, it++) {
-                    const int s = it % kS;
-                    // where a wait gives up, the rest of the walk waits no more and copies nothing
-                    const bool ok = mbar_wait(empty + s, ((it / kS) & 1) ^ 1, abort, p.err, p.wait_limit) && !*(volatile int *)abort;
-                    int page = -1;
-                    if (ok && walk.s.len > 0) page = kv4_page(p.c, walk.b, pg * SHERRY_KV4_PAGE, p.err);
-                    there[s] = page >= 0;
-                    if (page >= 0) {
-                        mbar_arrive_expect_tx(full + s, F::kStage);
-                        bulk_load(smem_u32(smem + s * F::kStage), kv4_block<D>(p.c, page, walk.h, 0), F::kStage, full + s);
-                    } else {
-                        mbar_arrive(full + s);
-                    }
-                }
-            }
-            // every copy lands before the CTA's shared memory is released
-            volatile int no_abort = 0;
-            for (uint32_t j = it < (uint32_t)kS ? 0 : it - kS; j < it; j++)
-                mbar_wait(full + j % kS, (j / kS) & 1, &no_abort, p.err, 1000000000LL);
-        }
-        return;
+    int copied = 0;
+    if (lane == 0) {
+        ahead = walk;
+        ahead.page1 = ahead_page = 0;
     }
+    auto copy_next = [&]() {
+        while (ahead_page >= ahead.page1) {
+            if (!ahead.next(p)) return;
+            ahead_page = ahead.page0;
+            if (ahead.s.len > p.c.width * SHERRY_KV4_PAGE) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
+        }
+        const int s = copied % kS;
+        const int page = ahead.s.len > 0 ? kv4_page(p.c, ahead.b, ahead_page * SHERRY_KV4_PAGE, p.err) : -1;
+        there[s] = page >= 0;
+        if (page >= 0) {
+            mbar_arrive_expect_tx(full + s, F::kStage);
+            bulk_load(smem_u32(ring + s * F::kStage), kv4_block<D>(p.c, page, ahead.h, 0), F::kStage, full + s);
+        } else {
+            mbar_arrive(full + s);
+        }
+        ahead_page++;
+        copied++;
+    };
+    if (lane == 0)
+        for (int s = 0; s < kS; s++) copy_next();
+    __syncwarp();
 
-    // ---------------- products ----------------
     const int r = lane >> 2, c = lane & 3;
     // Row m of a 16-token tile is token tok(m); chosen so that neither the keys' loads (a token per
     // four lanes) nor the values' (four tokens per lane) meet in a bank.
     const int tok_r = r ^ (r >> 2 & 1);                       // rows r and r + 8 (+ 8)
     const int tok_v0 = (2 * c) ^ (c >> 1 & 1), tok_v1 = (2 * c + 1) ^ (c >> 1 & 1);
+    const float scale = fabsf(p.scale2), lag = 8.0f / scale;  // a negative scale turns q's signs
+    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
     uint32_t it = 0;
+    bool dead = false;
     while (walk.next(p)) {
         const int nrow = walk.s.rows * p.g, row0 = walk.tile * kRows;
         const int pos0 = walk.s.len - walk.s.rows;            // position of the first new token
@@ -226,7 +244,6 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
         uint32_t qf[NT][MT][2];
         float qsum[NT][2];                                    // of rows 2 c, 2 c + 1
         int last[NT][2];                                      // last token those rows see
-        int last_min = 0x7FFFFFFF, last_max = -1;
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             const int row = row0 + 8 * t + r;
@@ -239,6 +256,7 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
             for (int w = 0; w < WK; w++) {
                 uint4 u = make_uint4(0, 0, 0, 0);
                 if (src) u = *reinterpret_cast<const uint4 *>(src + 8 * w);
+                u.x ^= flip, u.y ^= flip, u.z ^= flip, u.w ^= flip;
                 const uint32_t e[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int i = 0; i < 4; i++)
@@ -258,94 +276,115 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
                 last[t][j] = rw < nrow ? pos0 + rw / p.g : -1;
             }
         }
-        {
-            const int lo_row = row0, hi_row = min(row0 + kRows, nrow) - 1;
-            last_min = hi_row == row0 + kRows - 1 ? pos0 + lo_row / p.g : -1;  // rows past the end see nothing
-            last_max = pos0 + hi_row / p.g;
-        }
-        float o[NT][MT][4];
-        float m[NT][2], l[NT][2], corr[NT][2];
+        const int hi_row = min(row0 + kRows, nrow) - 1;
+        // rows past the end see nothing; their sums are dropped, so they need no mask
+        const int last_min = pos0 + row0 / p.g, last_max = pos0 + hi_row / p.g;
+        float o[NT][MT][4], ones[NT][4];                      // ones: sums of the rounded p s
+        // m: reference, in units before the scale; top: a score above it moves the reference
+        float m[NT][2], top[NT][2], l[NT][2], corr[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; t++) {
 #pragma unroll
-            for (int i = 0; i < MT; i++)
+            for (int j = 0; j < 4; j++) {
+                ones[t][j] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 4; j++) o[t][i][j] = 0.0f;
+                for (int i = 0; i < MT; i++) o[t][i][j] = 0.0f;
+            }
 #pragma unroll
-            for (int j = 0; j < 2; j++) m[t][j] = -INFINITY, l[t][j] = 0.0f, corr[t][j] = 0.0f;
+            for (int j = 0; j < 2; j++) m[t][j] = 0.0f, top[t][j] = -INFINITY, l[t][j] = 0.0f, corr[t][j] = 0.0f;
         }
         for (int pg = walk.page0; pg < walk.page1; pg++, it++) {
             const int s = it % kS;
-            const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, (it / kS) & 1, abort, p.err, p.wait_limit));
-            const int t0 = pg * SHERRY_KV4_PAGE + 16 * warp;  // first token of this warp's tile
-            if (ok && there[s] && t0 <= last_max) {
-                const uint8_t *kb = smem + s * F::kStage, *vb = kb + Kv4<D>::kBlock;
-                const int ta = 16 * warp + tok_r;             // rows r, r + 8 of the tile
-                uint32_t kw[2][WK];
+            dead = dead || !__all_sync(0xFFFFFFFFu, mbar_wait(full + s, (it / kS) & 1, abort, p.err, p.wait_limit));
+            const int t0 = pg * SHERRY_KV4_PAGE;              // first token of the page
+            if (!dead && there[s] && t0 <= last_max) {
+                const uint8_t *kb = ring + s * F::kStage, *vb = kb + Kv4<D>::kBlock;
+                const bool whole = t0 + SHERRY_KV4_PAGE - 1 <= last_min;
+#pragma unroll 1
+                for (int q0 = 0; q0 < 4; q0 += kTiles) {
+                float x[kTiles][NT][4];                       // scores of tiles of 16 tokens
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const uint8_t *src = kb + (ta + 8 * i) * Kv4<D>::kRow + c * (D / 8);
-                    if (D == 64) {
-                        const uint2 u = *reinterpret_cast<const uint2 *>(src);
-                        kw[i][0] = u.x, kw[i][1] = u.y;
-                    } else {
-                        const uint4 u = *reinterpret_cast<const uint4 *>(src);
-                        kw[i][0] = u.x, kw[i][1] = u.y;
-                        kw[i][WK - 2] = u.z, kw[i][WK - 1] = u.w;
+                for (int qi = 0; qi < kTiles; qi++) {
+                    const int q = q0 + qi;
+                    const int ta = 16 * q + tok_r;            // rows r, r + 8 of the tile
+                    uint32_t kw[2][WK];
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint8_t *src = kb + (ta + 8 * i) * Kv4<D>::kRow + c * (D / 8);
+                        if (D == 64) {
+                            const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                            kw[i][0] = u.x, kw[i][1] = u.y;
+                        } else {
+                            const uint4 u = *reinterpret_cast<const uint4 *>(src);
+                            kw[i][0] = u.x, kw[i][1] = u.y;
+                            kw[i][WK - 2] = u.z, kw[i][WK - 1] = u.w;
+                        }
                     }
-                }
-                const uint32_t *ksm = reinterpret_cast<const uint32_t *>(kb + Kv4<D>::kCodes) + ta;
-                const uint32_t *vsm = reinterpret_cast<const uint32_t *>(vb + Kv4<D>::kCodes) + ta;
-                const uint32_t kp[2] = {ksm[0], ksm[8]}, vp[2] = {vsm[0], vsm[8]};
-                float x[NT][4];
+                    const uint32_t *ksm = reinterpret_cast<const uint32_t *>(kb + Kv4<D>::kCodes) + ta;
+                    const uint32_t kp[2] = {ksm[0], ksm[8]};
 #pragma unroll
-                for (int t = 0; t < NT; t++) {
-                    x[t][0] = x[t][2] = -128.0f * qsum[t][0];
-                    x[t][1] = x[t][3] = -128.0f * qsum[t][1];
-                }
-#pragma unroll
-                for (int w = 0; w < WK; w++) {
-                    uint32_t a[4];
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        a[0] = code_pair(kw[0][w] >> (8 * k));
-                        a[1] = code_pair(kw[1][w] >> (8 * k));
-                        a[2] = code_pair(kw[0][w] >> (8 * k + 4));
-                        a[3] = code_pair(kw[1][w] >> (8 * k + 4));
-#pragma unroll
-                        for (int t = 0; t < NT; t++) mma_bf16(x[t], a, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
+                    for (int t = 0; t < NT; t++) {
+                        x[qi][t][0] = x[qi][t][2] = -128.0f * qsum[t][0];
+                        x[qi][t][1] = x[qi][t][3] = -128.0f * qsum[t][1];
                     }
+#pragma unroll
+                    for (int w = 0; w < WK; w++)
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const uint32_t a[4] = {code_pair(kw[0][w] >> (8 * k)), code_pair(kw[1][w] >> (8 * k)),
+                                                   code_pair(kw[0][w] >> (8 * k + 4)), code_pair(kw[1][w] >> (8 * k + 4))};
+#pragma unroll
+                            for (int t = 0; t < NT; t++) mma_bf16(x[qi][t], a, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
+                        }
+#pragma unroll
+                    for (int t = 0; t < NT; t++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++)
+#pragma unroll
+                            for (int j = 0; j < 2; j++)
+                                x[qi][t][2 * i + j] = kv4_step(kp[i]) * x[qi][t][2 * i + j] + kv4_low(kp[i]) * qsum[t][j];
                 }
-                const bool whole = t0 + 15 <= last_min;
+                if (!whole) {
+#pragma unroll
+                    for (int qi = 0; qi < kTiles; qi++)
+#pragma unroll
+                        for (int t = 0; t < NT; t++)
+#pragma unroll
+                            for (int j = 0; j < 4; j++)
+                                if (t0 + 16 * (q0 + qi) + tok_r + 8 * (j >> 1) > last[t][j & 1]) x[qi][t][j] = -INFINITY;
+                }
                 bool grow = false;
 #pragma unroll
                 for (int t = 0; t < NT; t++)
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const float sk = kv4_step(kp[i]) * p.scale2, mk = kv4_low(kp[i]) * p.scale2;
+                    for (int j = 0; j < 2; j++) {
+                        float mx = x[0][t][j];
 #pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            float v = sk * x[t][2 * i + j] + mk * qsum[t][j];
-                            if (!whole && t0 + tok_r + 8 * i > last[t][j]) v = -INFINITY;
-                            x[t][2 * i + j] = v;
-                            grow |= v > m[t][j] + 8.0f;
-                        }
+                        for (int k = 1; k < 2 * kTiles; k++) mx = fmaxf(mx, x[k >> 1][t][2 * (k & 1) + j]);
+                        grow |= mx > top[t][j];
                     }
                 // The reference of the exponentials follows the maximum only when a score exceeds it by
-                // 2^8: probabilities stay below 2^8, and most tiles skip the shuffles and the rescaling.
+                // 2^8: probabilities stay below 2^8, and most pages skip the shuffles and the rescaling.
                 if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
                     for (int t = 0; t < NT; t++)
 #pragma unroll
                         for (int j = 0; j < 2; j++) {
-                            float mx = fmaxf(m[t][j], fmaxf(x[t][j], x[t][2 + j]));
+                            float mx = x[0][t][j];
+#pragma unroll
+                            for (int k = 1; k < 2 * kTiles; k++) mx = fmaxf(mx, x[k >> 1][t][2 * (k & 1) + j]);
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-                            const float f = m[t][j] == -INFINITY ? 0.0f : exp2_fast(m[t][j] - mx);
+                            if (mx == -INFINITY) continue;
+                            const bool old = top[t][j] > -INFINITY;
+                            if (old) mx = fmaxf(mx, m[t][j]);
+                            const float f = old ? exp2_fast((m[t][j] - mx) * scale) : 0.0f;
                             m[t][j] = mx;
+                            top[t][j] = mx + lag;
                             l[t][j] *= f;
                             corr[t][j] *= f;
+                            ones[t][j] *= f;
 #pragma unroll
                             for (int i = 0; i < MT; i++) {
                                 o[t][i][j] *= f;
@@ -353,52 +392,59 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
                             }
                         }
                 }
-                uint32_t pb[NT][2];
 #pragma unroll
-                for (int t = 0; t < NT; t++)
+                for (int qi = 0; qi < kTiles; qi++) {
+                    const int q = q0 + qi;
+                    const uint32_t *vsm = reinterpret_cast<const uint32_t *>(vb + Kv4<D>::kCodes) + 16 * q + tok_r;
+                    const uint32_t vp[2] = {vsm[0], vsm[8]};
+                    uint32_t pb[NT][2];
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const float sv = kv4_step(vp[i]), cv = kv4_low(vp[i]) + 8.0f * sv;
-                        float ps[2];
+                    for (int t = 0; t < NT; t++)
 #pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            const float ref = m[t][j] == -INFINITY ? 0.0f : m[t][j];
-                            const float pr = exp2_fast(x[t][2 * i + j] - ref);
-                            const bool seen = whole || t0 + tok_r + 8 * i <= last[t][j];
-                            l[t][j] += pr;
-                            // a token that the row does not see may hold anything, NaN too
-                            ps[j] = seen ? pr * sv : 0.0f;
-                            corr[t][j] += seen ? pr * cv : 0.0f;
+                        for (int i = 0; i < 2; i++) {
+                            const float sv = kv4_step(vp[i]), cv = kv4_low(vp[i]) + 8.0f * sv;
+                            float ps[2];
+#pragma unroll
+                            for (int j = 0; j < 2; j++) {
+                                float pr = exp2_fast((x[qi][t][2 * i + j] - m[t][j]) * scale);
+                                float pc = pr * cv;
+                                ps[j] = pr * sv;
+                                if (!whole && t0 + 16 * q + tok_r + 8 * i > last[t][j])
+                                    pr = 0.0f, pc = 0.0f, ps[j] = 0.0f;  // it may hold anything, NaN too
+                                l[t][j] += pr;
+                                corr[t][j] += pc;
+                            }
+                            pb[t][i] = transpose8x8(pack_bf16(ps[0], ps[1]));
                         }
-                        const uint32_t u = pack_bf16(ps[0], ps[1]);
-                        corr[t][0] -= 136.0f * __uint_as_float(u << 16);
-                        corr[t][1] -= 136.0f * __uint_as_float(u & 0xFFFF0000u);
-                        pb[t][i] = transpose8x8(u);
+                    // values: lane (r, c) holds word(s) r of four tokens; a pair of tokens per register
+#pragma unroll
+                    for (int w = 0; w < D / 64; w++) {
+                        const uint8_t *src = vb + 16 * q * Kv4<D>::kRow + (r * (D / 64) + w) * 4;
+                        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(src + tok_v0 * Kv4<D>::kRow);
+                        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(src + tok_v1 * Kv4<D>::kRow);
+                        const uint32_t w2 = *reinterpret_cast<const uint32_t *>(src + (tok_v0 + 8) * Kv4<D>::kRow);
+                        const uint32_t w3 = *reinterpret_cast<const uint32_t *>(src + (tok_v1 + 8) * Kv4<D>::kRow);
+                        const uint32_t al = prmt(w0, w1, 0x5410), ah = prmt(w0, w1, 0x7632);
+                        const uint32_t bl = prmt(w2, w3, 0x5410), bh = prmt(w2, w3, 0x7632);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const uint32_t a[4] = {code_pair(al >> (4 * i)), code_pair(ah >> (4 * i)),
+                                                   code_pair(bl >> (4 * i)), code_pair(bh >> (4 * i))};
+#pragma unroll
+                            for (int t = 0; t < NT; t++) mma_bf16(o[t][4 * w + i], a, pb[t][0], pb[t][1]);
+                        }
                     }
-                // values: lane (r, c) holds word(s) r of four tokens; a pair of tokens per register
+                    const uint32_t a1[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-                for (int w = 0; w < D / 64; w++) {
-                    const uint8_t *src = vb + 16 * warp * Kv4<D>::kRow + (r * (D / 64) + w) * 4;
-                    const uint32_t w0 = *reinterpret_cast<const uint32_t *>(src + tok_v0 * Kv4<D>::kRow);
-                    const uint32_t w1 = *reinterpret_cast<const uint32_t *>(src + tok_v1 * Kv4<D>::kRow);
-                    const uint32_t w2 = *reinterpret_cast<const uint32_t *>(src + (tok_v0 + 8) * Kv4<D>::kRow);
-                    const uint32_t w3 = *reinterpret_cast<const uint32_t *>(src + (tok_v1 + 8) * Kv4<D>::kRow);
-                    const uint32_t al = prmt(w0, w1, 0x5410), ah = prmt(w0, w1, 0x7632);
-                    const uint32_t bl = prmt(w2, w3, 0x5410), bh = prmt(w2, w3, 0x7632);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint32_t a[4] = {code_pair(al >> (4 * i)), code_pair(ah >> (4 * i)),
-                                               code_pair(bl >> (4 * i)), code_pair(bh >> (4 * i))};
-#pragma unroll
-                        for (int t = 0; t < NT; t++) mma_bf16(o[t][4 * w + i], a, pb[t][0], pb[t][1]);
-                    }
+                    for (int t = 0; t < NT; t++) mma_bf16(ones[t], a1, pb[t][0], pb[t][1]);
+                }
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty + s);
+            if (lane == 0 && !dead) copy_next();
         }
 
-        // ---------------- the four warps' sums together ----------------
+        // ---------------- the piece's result ----------------
 #pragma unroll
         for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -408,122 +454,83 @@ __global__ void __launch_bounds__(kFewThreads) attn_few_kernel(const __grid_cons
                     l[t][j] += __shfl_xor_sync(0xFFFFFFFFu, l[t][j], k);
                     corr[t][j] += __shfl_xor_sync(0xFFFFFFFFu, corr[t][j], k);
                 }
-                if (r == 0) stat[warp * kRows + 8 * t + 2 * c + j] = m[t][j];
+                corr[t][j] -= 136.0f * ones[t][j];
             }
-        few_sync();
-        float mx[NT][2];
+        const bool all = walk.page0 == 0 && walk.page1 == walk.s.pages;
+        // parts of a row tile: slot 1 of the run that holds its first page, slot 0 of the others
+        const long long slot = 2LL * run + (walk.page0 == 0 ? 1 : 0);
 #pragma unroll
         for (int t = 0; t < NT; t++)
 #pragma unroll
             for (int j = 0; j < 2; j++) {
-                const int row = 8 * t + 2 * c + j;
-                float v = stat[row];
+                const int row = 8 * t + 2 * c + j, rw = row0 + row;
+                if (rw >= nrow) continue;
+                const float cr = corr[t][j];
+                if (all) {
+                    const float inv = l[t][j] == 0.0f ? 0.0f : 1.0f / l[t][j];
+                    uint16_t *dst = p.out + (long long)(walk.s.first + rw / p.g) * p.out_stride +
+                                    (long long)(walk.h * p.g + rw % p.g) * D + r * (D / 8);
 #pragma unroll
-                for (int w = 1; w < kFewWarps; w++) v = fmaxf(v, stat[w * kRows + row]);
-                mx[t][j] = v;
-                const float f = m[t][j] == -INFINITY ? 0.0f : exp2_fast(m[t][j] - v);
-                // a NaN score leaves m at -inf but reaches l: keep it
-                l[t][j] = m[t][j] == -INFINITY && l[t][j] == 0.0f ? 0.0f : l[t][j] * (m[t][j] == -INFINITY ? 1.0f : f);
-                corr[t][j] *= f;
+                    for (int i = 0; i < MT; i += 4) {
+                        float v[8];  // elements 2 i ... 2 i + 7 of the lane's D / 8
 #pragma unroll
-                for (int i = 0; i < MT; i++) {
-                    o[t][i][j] = (o[t][i][j] * f) + corr[t][j];
-                    o[t][i][2 + j] = (o[t][i][2 + j] * f) + corr[t][j];
+                        for (int k = 0; k < 8; k++) v[k] = (o[t][i + (k & 3)][2 * (k >> 2) + j] + cr) * inv;
+                        *reinterpret_cast<uint4 *>(dst + 2 * i) =
+                            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+                    }
+                } else {
+                    float *dst = p.ws + (slot * kRows + row) * D + r * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < MT; i += 4)
+#pragma unroll
+                        for (int k = 0; k < 2; k++)
+                            *reinterpret_cast<float4 *>(dst + 2 * i + 4 * k) =
+                                make_float4(o[t][i][2 * k + j] + cr, o[t][i + 1][2 * k + j] + cr, o[t][i + 2][2 * k + j] + cr,
+                                            o[t][i + 3][2 * k + j] + cr);
+                    if (r == 0)
+                        reinterpret_cast<float2 *>(p.ws + 2LL * p.grid * kRows * D)[slot * kRows + row] =
+                            make_float2(top[t][j] == -INFINITY ? -INFINITY : m[t][j] * scale, l[t][j]);
                 }
             }
-        float *sums = stat + 4 * kRows;
-        for (int w = 0; w < kFewWarps; w++) {
-            if (w == warp) {
-#pragma unroll
-                for (int t = 0; t < NT; t++)
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        const int row = 8 * t + 2 * c + j;
-                        float *dst = join + row * D + r * (D / 8);
-#pragma unroll
-                        for (int i = 0; i < MT; i += 4)
-#pragma unroll
-                            for (int k = 0; k < 2; k++) {
-                                // elements 8 word + 4 k + 0 .. 3
-                                float4 v = make_float4(o[t][i][2 * k + j], o[t][i + 1][2 * k + j],
-                                                       o[t][i + 2][2 * k + j], o[t][i + 3][2 * k + j]);
-                                float4 *d4 = reinterpret_cast<float4 *>(dst + 2 * i + 4 * k);
-                                if (w > 0) {
-                                    const float4 u = *d4;
-                                    v = make_float4(u.x + v.x, u.y + v.y, u.z + v.z, u.w + v.w);
-                                }
-                                *d4 = v;
-                            }
-                        if (r == 0) sums[row] = w == 0 ? l[t][j] : sums[row] + l[t][j];
-                    }
-            }
-            few_sync();
-        }
-        // whole: the result; else this run's part to the workspace
-        const bool all = walk.page0 == 0 && walk.page1 == walk.s.pages;
-        const int tid = threadIdx.x;
-        if (all) {
-            for (int i = tid; i < kRows * (D / 8); i += 32 * kFewWarps) {
-                const int row = i / (D / 8), d = (i % (D / 8)) * 8, rw = row0 + row;
-                if (rw >= nrow) continue;
-                const float sum = sums[row];
-                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                const float4 a = *reinterpret_cast<const float4 *>(join + row * D + d);
-                const float4 b = *reinterpret_cast<const float4 *>(join + row * D + d + 4);
-                uint16_t *dst = p.out + (long long)(walk.s.first + rw / p.g) * p.out_stride +
-                                (long long)(walk.h * p.g + rw % p.g) * D + d;
-                *reinterpret_cast<uint4 *>(dst) =
-                    make_uint4(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv),
-                               pack_bf16(b.x * inv, b.y * inv), pack_bf16(b.z * inv, b.w * inv));
-            }
-        } else {
-            // the piece that began before this run takes slot 0, one that begins inside it slot 1
-            const long long begin = walk.w - walk.page1;      // the unit's first page
-            const long long slot = 2LL * blockIdx.x + (begin > from ? 1 : 0);
-            float4 *dst = reinterpret_cast<float4 *>(p.ws + slot * kRows * D);
-            for (int i = tid; i < kRows * D / 4; i += 32 * kFewWarps) dst[i] = reinterpret_cast<const float4 *>(join)[i];
-            if (r == 0 && warp == 0) {
-                float2 *ml = reinterpret_cast<float2 *>(p.ws + 2LL * p.grid * kRows * D) + slot * kRows;
-#pragma unroll
-                for (int t = 0; t < NT; t++)
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        const int row = 8 * t + 2 * c + j;
-                        ml[row] = make_float2(mx[t][j], sums[row]);
-                    }
-            }
-        }
-        few_sync();  // join and stat are free for the next piece
+    }
+    if (dead && lane == 0) {
+        // copies in flight land before the CTA's shared memory is released
+        volatile int no_abort = 0;
+        for (int j = max((int)it, copied - kS); j < copied; j++)
+            mbar_wait(full + j % kS, (j / kS) & 1, &no_abort, p.err, 1000000000LL);
     }
 }
 
-// Joins the parts of the row tiles that the runs cut: CTA i takes the one that begins in run i and
-// goes on in the next, one warp per row, its parts in the order of the CTAs.
+// Joins the parts of the row tiles that the runs cut: a CTA per row tile, a warp per row, the parts in the
+// order of the runs.
 template <int D, int NT>
 __global__ void __launch_bounds__(256 * NT, 2) attn_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kRows = 8 * NT, E = D / 32;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const long long W = all_units<kRows>(p);
-    const int n = (int)min((long long)p.grid, W), i0 = blockIdx.x;
-    if (i0 >= n - 1) return;
-    const long long from = run_start(W, i0, n), to = run_start(W, i0 + 1, n);
+    const Work work = all_work<kRows>(p);
     int b;
-    long long before;
-    find_unit<kRows>(p, to - 1, b, before);
+    long long units, before;
+    find_seq<kRows, true>(p, work, blockIdx.x, b, units);
     if (b >= p.c.B) return;
     const SeqWork s = seq_work<kRows>(p, b);
-    const int unit = (int)((to - 1 - before) / s.pages);
-    const long long w0 = before + (long long)unit * s.pages, w1 = w0 + s.pages;
-    if (w1 <= to || w0 < from) return;  // not cut here, or begun by an earlier CTA
+    const int unit = (int)(blockIdx.x - units);
+    before = 0;
+    for (int i = lane; i < b; i += 32) {
+        const SeqWork t = seq_work<kRows>(p, i);
+        before += (long long)p.c.H * t.tiles * (t.pages + work.cost);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     const int h = unit / s.tiles, rw = (unit - h * s.tiles) * kRows + row;
     if (rw >= s.rows * p.g) return;
-    const int i1 = run_of(W, w1 - 1, n);
+    const long long x0 = before + (long long)unit * (s.pages + work.cost) + work.cost;  // the first page's place
+    const int i0 = run_of(work, x0), i1 = run_of(work, x0 + s.pages - 1);
+    if (i0 == i1) return;  // one run held all of it and wrote the result
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws + 2LL * p.grid * kRows * D);
-    const int first_slot = w0 > from ? 1 : 0;
     float m = -INFINITY;
-    for (int i = i0 + lane; i <= i1; i += 32) m = fmaxf(m, ml[(2LL * i + (i == i0 ? first_slot : 0)) * kRows + row].x);
+    for (int i = i0 + lane; i <= i1; i += 32) m = fmaxf(m, ml[(2LL * i + (i == i0)) * kRows + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     float l = 0.0f, acc[E];
@@ -533,16 +540,16 @@ __global__ void __launch_bounds__(256 * NT, 2) attn_join_kernel(const __grid_con
         const int i = ib + lane;
         float f = 0.0f;
         if (i <= i1) {
-            const float2 v = ml[(2LL * i + (i == i0 ? first_slot : 0)) * kRows + row];
+            const float2 v = ml[(2LL * i + (i == i0)) * kRows + row];
             // a part without keys has sum 0; a NaN among its scores shows in the sum
             f = v.x == -INFINITY ? (v.y == 0.0f ? 0.0f : v.y) : exp2_fast(v.x - m);
             l += v.y * f;
         }
         const int k1 = min(32, i1 - ib + 1);
-#pragma unroll 8
+#pragma unroll 16
         for (int k = 0; k < k1; k++) {
             const float fk = __shfl_sync(0xFFFFFFFFu, f, k);
-            const long long slot = 2LL * (ib + k) + (ib + k == i0 ? first_slot : 0);
+            const long long slot = 2LL * (ib + k) + (ib + k == i0);
             const float *src = p.ws + (slot * kRows + row) * D + lane * E;
             if (E == 2) {
                 const float2 v = *reinterpret_cast<const float2 *>(src);
@@ -599,23 +606,31 @@ sherry_status few_launch(AttnParams p, cudaStream_t stream) {
     using F = Few<D, NT>;
     static OccupancyCache cache;
     const int bps = few_blocks_per_sm(attn_few_kernel<D, NT>, F::kSmem, cache);
-    p.grid = std::min(sm_count() * bps, kFewCtasMax);
-    launch_after(attn_few_kernel<D, NT>, dim3((unsigned)p.grid), kFewThreads, F::kSmem, stream, p);
+    const int ctas = std::min(sm_count() * bps, kFewRunsMax / kFewWarps);
+    p.grid = ctas * kFewWarps;  // runs
+    launch_after(attn_few_kernel<D, NT>, dim3((unsigned)ctas), kFewThreads, F::kSmem, stream, p);
     const sherry_status st = launch_status("sherry_attn_kv4");
     // a table of one page cuts nothing
     if (st != SHERRY_OK || p.c.width == 1) return st;
-    launch_after(attn_join_kernel<D, NT>, dim3((unsigned)p.grid), 256 * NT, 0, stream, p);
+    // at most this many row tiles
+    long long tiles = (long long)p.c.T * p.g / F::kRows + p.c.B;
+    if (p.few_rows < 0x7FFFFFFF)
+        tiles = std::min(tiles, (long long)p.c.B * ((p.few_rows + F::kRows - 1) / F::kRows));
+    if (!p.c.cu) tiles = (long long)p.c.B * ((p.g + F::kRows - 1) / F::kRows);
+    tiles *= p.c.H;
+    if (tiles > 0x7FFFFFFF) return SHERRY_ERR_UNSUPPORTED;
+    launch_after(attn_join_kernel<D, NT>, dim3((unsigned)tiles), 256 * NT, 0, stream, p);
     return launch_status("sherry_attn_kv4 (join)");
 }
 
 }  // namespace
 }  // namespace sherry
 
-// The parts of the row tiles that the runs of the few-row kernel cut: at most two per CTA, each
+// The parts of the row tiles that the runs of the few-row kernel cut: at most two per run, each
 // with 16 rows of D sums, a maximum and a total.
 extern "C" size_t sherry_attn_kv4_workspace_bytes(int64_t T, int Hq, int D) {
     if (T < 1 || Hq < 1 || (D != 64 && D != 128)) return 0;
-    return (size_t)2 * sherry::kFewCtasMax * 16 * (size_t)(D + 2) * 4;
+    return (size_t)2 * sherry::kFewRunsMax * 16 * (size_t)(D + 2) * 4;
 }
 
 extern "C" sherry_status sherry_attn_kv4(const sherry_kv4 *c, const uint16_t *q, int64_t q_stride, uint16_t *out,

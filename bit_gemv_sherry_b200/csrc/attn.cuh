@@ -25,7 +25,7 @@ struct AttnParams {
     long long q_stride, out_stride;
     long long wait_limit;
     int g;              // query heads per key/value head
-    int grid;           // few rows: CTAs
+    int grid;           // few rows: runs
     int few_rows;       // sequences with more rows (new tokens times g) are the tile kernel's
     float scale2;       // scale * log2(e)
     unsigned int *err;

@@ -18,11 +18,14 @@ namespace {
 // timing).  A warp works alone: it copies its pages into its own ring (a page's keys and values are one
 // contiguous block: one bulk copy), and no other warp waits for it.
 // The product is S^T = K q^T, 16 tokens by 8 rows: the 8-wide side carries the few rows, so 4 query heads
-// per key/value head fill half of the instruction instead of a quarter.  The 128 of the codes' bf16 is
-// taken out of the first product by starting it at -128 sum(q), and out of the second by -136 times the
-// sum of the rounded p s, which one more product with ones gives.
-// Earlier form: a page shared by four warps, 16 tokens each, filled by a fifth: 1,520 instructions a page
-// of heads of 64 against about 600 here, and 357 us for 32 sequences of 32,768 tokens.
+// per key/value head fill half of the instruction instead of a quarter.
+// Decoding is what bounds it next (integer instructions, half of an SM's rate): a code's four bits at the
+// bottom of a half word are the fp16 c 2^-24, one up c 2^-20, so a word of eight codes takes a shift and
+// four ANDs; the powers of two go into q (fp16, exact after a power of two per row) and into the last
+// factor of the result.
+// Earlier forms, 32 sequences of 32,768 tokens with heads of 128 (floor 177 us): a page shared by four
+// warps and filled by a fifth, 357 us; a warp per page with codes as bf16 128 + c (a shift and an OR
+// more per pair), 320 us.
 constexpr int kFewWarps = 4;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewRunsMax = 2560;  // bounds the workspace
@@ -158,9 +161,9 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
         " {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -171,6 +174,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
     return d;
 }
+
+// A probability of 1 times the largest step is held as about 2^kUp: fp16 has room for references that lag
+// by 2^8, and 2^-21 of the largest still has its 11 bits.
+constexpr float kUp = 7.0f;
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_kernel(const __grid_constant__ AttnParams p) {
@@ -233,45 +242,61 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
     // four lanes) nor the values' (four tokens per lane) meet in a bank.
     const int tok_r = r ^ (r >> 2 & 1);                       // rows r and r + 8 (+ 8)
     const int tok_v0 = (2 * c) ^ (c >> 1 & 1), tok_v1 = (2 * c + 1) ^ (c >> 1 & 1);
-    const float scale = fabsf(p.scale2), lag = 8.0f / scale;  // a negative scale turns q's signs
-    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;  // a negative scale turns q's signs
     uint32_t it = 0;
     bool dead = false;
     while (walk.next(p)) {
         const int nrow = walk.s.rows * p.g, row0 = walk.tile * kRows;
         const int pos0 = walk.s.len - walk.s.rows;            // position of the first new token
         // q: lane (r, c) holds elements [c D / 4, (c + 1) D / 4) of row r of each row group
+        // as fp16 of q 2^-e, the odd nibbles' elements 2^-4 of it again
         uint32_t qf[NT][MT][2];
-        float qsum[NT][2];                                    // of rows 2 c, 2 c + 1
+        float qsum[NT][2], sc[NT][2];                         // of rows 2 c, 2 c + 1: sum(q), scale of a score
         int last[NT][2];                                      // last token those rows see
 #pragma unroll
         for (int t = 0; t < NT; t++) {
             const int row = row0 + 8 * t + r;
-            float sum = 0.0f;
+            float sum = 0.0f, most = 0.0f;
             const uint16_t *src = nullptr;
             if (row < nrow)
                 src = p.q + (long long)(walk.s.first + row / p.g) * p.q_stride +
                       (long long)(walk.h * p.g + row % p.g) * D + c * (D / 4);
+            uint4 u[WK];
 #pragma unroll
             for (int w = 0; w < WK; w++) {
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (src) u = *reinterpret_cast<const uint4 *>(src + 8 * w);
-                u.x ^= flip, u.y ^= flip, u.z ^= flip, u.w ^= flip;
-                const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+                u[w] = make_uint4(0, 0, 0, 0);
+                if (src) u[w] = *reinterpret_cast<const uint4 *>(src + 8 * w);
+                u[w].x ^= flip, u[w].y ^= flip, u[w].z ^= flip, u[w].w ^= flip;
+                const uint32_t e[4] = {u[w].x, u[w].y, u[w].z, u[w].w};
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    sum += __uint_as_float(e[i] << 16) + __uint_as_float(e[i] & 0xFFFF0000u);
-                // a code word's pairs are elements (i, i + 4)
-                qf[t][2 * w][0] = prmt(u.x, u.z, 0x5410);
-                qf[t][2 * w][1] = prmt(u.x, u.z, 0x7632);
-                qf[t][2 * w + 1][0] = prmt(u.y, u.w, 0x5410);
-                qf[t][2 * w + 1][1] = prmt(u.y, u.w, 0x7632);
+                for (int i = 0; i < 4; i++) {
+                    const float lo = __uint_as_float(e[i] << 16), hi = __uint_as_float(e[i] & 0xFFFF0000u);
+                    sum += lo + hi;
+                    most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
+                }
             }
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+            const int e = max((int)(__float_as_uint(most) >> 23) - 127 - 13, -100);  // the largest below 2^14
+            const float d0 = pow2(-e), d1 = d0 * 0.0625f;
+#pragma unroll
+            for (int w = 0; w < WK; w++) {
+                // a code word's pairs are elements (i, i + 4)
+                const uint32_t lo[2] = {u[w].x, u[w].y}, hi[2] = {u[w].z, u[w].w};
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    qf[t][2 * w + k][0] = pack_f16(__uint_as_float(lo[k] << 16) * d0, __uint_as_float(hi[k] << 16) * d0);
+                    qf[t][2 * w + k][1] =
+                        pack_f16(__uint_as_float(lo[k] & 0xFFFF0000u) * d1, __uint_as_float(hi[k] & 0xFFFF0000u) * d1);
+                }
+            }
+            sum *= d0 * 5.9604644775390625e-08f;              // 2^-24: in units of the product
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 qsum[t][j] = __shfl_sync(0xFFFFFFFFu, sum, (2 * c + j) * 4);
+                sc[t][j] = fabsf(p.scale2) * pow2(24 + __shfl_sync(0xFFFFFFFFu, e, (2 * c + j) * 4));
                 const int rw = row0 + 8 * t + 2 * c + j;
                 last[t][j] = rw < nrow ? pos0 + rw / p.g : -1;
             }
@@ -279,19 +304,20 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
         const int hi_row = min(row0 + kRows, nrow) - 1;
         // rows past the end see nothing; their sums are dropped, so they need no mask
         const int last_min = pos0 + row0 / p.g, last_max = pos0 + hi_row / p.g;
-        float o[NT][MT][4], ones[NT][4];                      // ones: sums of the rounded p s
-        // m: reference, in units before the scale; top: a score above it moves the reference
-        float m[NT][2], top[NT][2], l[NT][2], corr[NT][2];
+        // All sums are of 2^(x - m) 2^(kUp - ve): m is the row's reference (x in units before the scale), ve
+        // a power of two above the values' steps, and ref = m sc - (kUp - ve).
+        float o[NT][MT][4];
+        float m[NT][2], ref[NT][2], l[NT][2], corr[NT][2];
+        int ve = -100;
+        float step_top = pow2(ve), sum_top = pow2(15 - ve);   // a step, a sum of probabilities above it moves them
 #pragma unroll
         for (int t = 0; t < NT; t++) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                ones[t][j] = 0.0f;
+            for (int i = 0; i < MT; i++)
 #pragma unroll
-                for (int i = 0; i < MT; i++) o[t][i][j] = 0.0f;
-            }
+                for (int j = 0; j < 4; j++) o[t][i][j] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 2; j++) m[t][j] = 0.0f, top[t][j] = -INFINITY, l[t][j] = 0.0f, corr[t][j] = 0.0f;
+            for (int j = 0; j < 2; j++) m[t][j] = -INFINITY, ref[t][j] = 0.0f, l[t][j] = 0.0f, corr[t][j] = 0.0f;
         }
         for (int pg = walk.page0; pg < walk.page1; pg++, it++) {
             const int s = it % kS;
@@ -323,18 +349,15 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                     const uint32_t *ksm = reinterpret_cast<const uint32_t *>(kb + Kv4<D>::kCodes) + ta;
                     const uint32_t kp[2] = {ksm[0], ksm[8]};
 #pragma unroll
-                    for (int t = 0; t < NT; t++) {
-                        x[qi][t][0] = x[qi][t][2] = -128.0f * qsum[t][0];
-                        x[qi][t][1] = x[qi][t][3] = -128.0f * qsum[t][1];
-                    }
+                    for (int t = 0; t < NT; t++) x[qi][t][0] = x[qi][t][1] = x[qi][t][2] = x[qi][t][3] = 0.0f;
 #pragma unroll
                     for (int w = 0; w < WK; w++)
 #pragma unroll
                         for (int k = 0; k < 2; k++) {
-                            const uint32_t a[4] = {code_pair(kw[0][w] >> (8 * k)), code_pair(kw[1][w] >> (8 * k)),
-                                                   code_pair(kw[0][w] >> (8 * k + 4)), code_pair(kw[1][w] >> (8 * k + 4))};
+                            const uint32_t u0 = kw[0][w] >> (8 * k), u1 = kw[1][w] >> (8 * k);
+                            const uint32_t a[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
 #pragma unroll
-                            for (int t = 0; t < NT; t++) mma_bf16(x[qi][t], a, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
+                            for (int t = 0; t < NT; t++) mma_f16(x[qi][t], a, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
                         }
 #pragma unroll
                     for (int t = 0; t < NT; t++)
@@ -344,28 +367,73 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                             for (int j = 0; j < 2; j++)
                                 x[qi][t][2 * i + j] = kv4_step(kp[i]) * x[qi][t][2 * i + j] + kv4_low(kp[i]) * qsum[t][j];
                 }
+                float sv[kTiles][2], mv[kTiles][2];           // steps and low ends of the values
+#pragma unroll
+                for (int qi = 0; qi < kTiles; qi++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint32_t vp = reinterpret_cast<const uint32_t *>(vb + Kv4<D>::kCodes)[16 * (q0 + qi) + tok_r + 8 * i];
+                        sv[qi][i] = kv4_step(vp);
+                        mv[qi][i] = kv4_low(vp);
+                    }
                 if (!whole) {
+                    // a token that a row does not see may hold anything, NaN too
+#pragma unroll
+                    for (int qi = 0; qi < kTiles; qi++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const int tok = t0 + 16 * (q0 + qi) + tok_r + 8 * i;
+                            if (tok > last_max) sv[qi][i] = mv[qi][i] = 0.0f;
+#pragma unroll
+                            for (int t = 0; t < NT; t++)
+#pragma unroll
+                                for (int j = 0; j < 2; j++)
+                                    if (tok > last[t][j]) x[qi][t][2 * i + j] = -INFINITY;
+                        }
+                }
+                float step = fmaxf(sv[0][0], sv[0][1]);
+#pragma unroll
+                for (int qi = 1; qi < kTiles; qi++) step = fmaxf(step, fmaxf(sv[qi][0], sv[qi][1]));
+                uint32_t pb[kTiles][NT][2];
+                float sum[NT][2], csum[NT][2];
+                // The references follow the maximum only when probabilities grow out of fp16: most pages skip the
+                // shuffles and the rescaling.
+                for (bool moved = false;; moved = true) {
+                    bool grow = step > step_top;
+#pragma unroll
+                    for (int t = 0; t < NT; t++)
+#pragma unroll
+                        for (int j = 0; j < 2; j++) sum[t][j] = csum[t][j] = 0.0f;
 #pragma unroll
                     for (int qi = 0; qi < kTiles; qi++)
 #pragma unroll
                         for (int t = 0; t < NT; t++)
 #pragma unroll
-                            for (int j = 0; j < 4; j++)
-                                if (t0 + 16 * (q0 + qi) + tok_r + 8 * (j >> 1) > last[t][j & 1]) x[qi][t][j] = -INFINITY;
-                }
-                bool grow = false;
+                            for (int i = 0; i < 2; i++) {
+                                float ps[2];
 #pragma unroll
-                for (int t = 0; t < NT; t++)
+                                for (int j = 0; j < 2; j++) {
+                                    float pr = exp2_fast(x[qi][t][2 * i + j] * sc[t][j] - ref[t][j]);
+                                    float pm = pr * mv[qi][i];
+                                    ps[j] = pr * sv[qi][i];
+                                    if (!whole && x[qi][t][2 * i + j] == -INFINITY) pr = pm = ps[j] = 0.0f;
+                                    sum[t][j] += pr;
+                                    csum[t][j] += pm;
+                                }
+                                pb[qi][t][i] = pack_f16(ps[0], ps[1]);
+                            }
 #pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        float mx = x[0][t][j];
+                    for (int t = 0; t < NT; t++)
 #pragma unroll
-                        for (int k = 1; k < 2 * kTiles; k++) mx = fmaxf(mx, x[k >> 1][t][2 * (k & 1) + j]);
-                        grow |= mx > top[t][j];
-                    }
-                // The reference of the exponentials follows the maximum only when a score exceeds it by
-                // 2^8: probabilities stay below 2^8, and most pages skip the shuffles and the rescaling.
-                if (__any_sync(0xFFFFFFFFu, grow)) {
+                        for (int j = 0; j < 2; j++)
+                            grow |= sum[t][j] > sum_top || (m[t][j] == -INFINITY && (whole || t0 + 16 * q0 <= last[t][j]));
+                    // once is enough (a row of nothing but NaN has no reference after it either)
+                    if (moved || !__any_sync(0xFFFFFFFFu, grow)) break;
+                    const int old = ve;
+                    const float most = step < INFINITY ? fmaxf(step, 0.0f) : 0.0f;
+                    ve = max(ve, min((int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)) >> 23) - 126, 100));
+                    step_top = pow2(ve);
+                    sum_top = pow2(15 - ve);
 #pragma unroll
                     for (int t = 0; t < NT; t++)
 #pragma unroll
@@ -376,15 +444,12 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-                            if (mx == -INFINITY) continue;
-                            const bool old = top[t][j] > -INFINITY;
-                            if (old) mx = fmaxf(mx, m[t][j]);
-                            const float f = old ? exp2_fast((m[t][j] - mx) * scale) : 0.0f;
+                            mx = fmaxf(mx, m[t][j]);
+                            const float f = m[t][j] == -INFINITY ? 0.0f : exp2_fast((m[t][j] - mx) * sc[t][j] + (float)(old - ve));
                             m[t][j] = mx;
-                            top[t][j] = mx + lag;
+                            ref[t][j] = (mx == -INFINITY ? 0.0f : mx * sc[t][j]) - (kUp - (float)ve);
                             l[t][j] *= f;
                             corr[t][j] *= f;
-                            ones[t][j] *= f;
 #pragma unroll
                             for (int i = 0; i < MT; i++) {
                                 o[t][i][j] *= f;
@@ -393,29 +458,19 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                         }
                 }
 #pragma unroll
+                for (int t = 0; t < NT; t++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        l[t][j] += sum[t][j];
+                        corr[t][j] += csum[t][j];
+                    }
+#pragma unroll
                 for (int qi = 0; qi < kTiles; qi++) {
                     const int q = q0 + qi;
-                    const uint32_t *vsm = reinterpret_cast<const uint32_t *>(vb + Kv4<D>::kCodes) + 16 * q + tok_r;
-                    const uint32_t vp[2] = {vsm[0], vsm[8]};
-                    uint32_t pb[NT][2];
 #pragma unroll
                     for (int t = 0; t < NT; t++)
 #pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const float sv = kv4_step(vp[i]), cv = kv4_low(vp[i]) + 8.0f * sv;
-                            float ps[2];
-#pragma unroll
-                            for (int j = 0; j < 2; j++) {
-                                float pr = exp2_fast((x[qi][t][2 * i + j] - m[t][j]) * scale);
-                                float pc = pr * cv;
-                                ps[j] = pr * sv;
-                                if (!whole && t0 + 16 * q + tok_r + 8 * i > last[t][j])
-                                    pr = 0.0f, pc = 0.0f, ps[j] = 0.0f;  // it may hold anything, NaN too
-                                l[t][j] += pr;
-                                corr[t][j] += pc;
-                            }
-                            pb[t][i] = transpose8x8(pack_bf16(ps[0], ps[1]));
-                        }
+                        for (int i = 0; i < 2; i++) pb[qi][t][i] = transpose8x8(pb[qi][t][i]);
                     // values: lane (r, c) holds word(s) r of four tokens; a pair of tokens per register
 #pragma unroll
                     for (int w = 0; w < D / 64; w++) {
@@ -428,15 +483,13 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                         const uint32_t bl = prmt(w2, w3, 0x5410), bh = prmt(w2, w3, 0x7632);
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
-                            const uint32_t a[4] = {code_pair(al >> (4 * i)), code_pair(ah >> (4 * i)),
-                                                   code_pair(bl >> (4 * i)), code_pair(bh >> (4 * i))};
+                            const uint32_t mask = i & 1 ? 0x00F000F0u : 0x000F000Fu;
+                            const int sh = 8 * (i >> 1);
+                            const uint32_t a[4] = {(al >> sh) & mask, (ah >> sh) & mask, (bl >> sh) & mask, (bh >> sh) & mask};
 #pragma unroll
-                            for (int t = 0; t < NT; t++) mma_bf16(o[t][4 * w + i], a, pb[t][0], pb[t][1]);
+                            for (int t = 0; t < NT; t++) mma_f16(o[t][4 * w + i], a, pb[qi][t][0], pb[qi][t][1]);
                         }
                     }
-                    const uint32_t a1[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-#pragma unroll
-                    for (int t = 0; t < NT; t++) mma_bf16(ones[t], a1, pb[t][0], pb[t][1]);
                 }
                 }
             }
@@ -454,7 +507,12 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                     l[t][j] += __shfl_xor_sync(0xFFFFFFFFu, l[t][j], k);
                     corr[t][j] += __shfl_xor_sync(0xFFFFFFFFu, corr[t][j], k);
                 }
-                corr[t][j] -= 136.0f * ones[t][j];
+#pragma unroll
+                for (int i = 0; i < MT; i++) {
+                    const float f = i & 1 ? 1048576.0f : 16777216.0f;  // the codes' 2^-20 and 2^-24
+                    o[t][i][j] = o[t][i][j] * f + corr[t][j];
+                    o[t][i][2 + j] = o[t][i][2 + j] * f + corr[t][j];
+                }
             }
         const bool all = walk.page0 == 0 && walk.page1 == walk.s.pages;
         // parts of a row tile: slot 1 of the run that holds its first page, slot 0 of the others
@@ -465,7 +523,6 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             for (int j = 0; j < 2; j++) {
                 const int row = 8 * t + 2 * c + j, rw = row0 + row;
                 if (rw >= nrow) continue;
-                const float cr = corr[t][j];
                 if (all) {
                     const float inv = l[t][j] == 0.0f ? 0.0f : 1.0f / l[t][j];
                     uint16_t *dst = p.out + (long long)(walk.s.first + rw / p.g) * p.out_stride +
@@ -474,7 +531,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                     for (int i = 0; i < MT; i += 4) {
                         float v[8];  // elements 2 i ... 2 i + 7 of the lane's D / 8
 #pragma unroll
-                        for (int k = 0; k < 8; k++) v[k] = (o[t][i + (k & 3)][2 * (k >> 2) + j] + cr) * inv;
+                        for (int k = 0; k < 8; k++) v[k] = o[t][i + (k & 3)][2 * (k >> 2) + j] * inv;
                         *reinterpret_cast<uint4 *>(dst + 2 * i) =
                             make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
                     }
@@ -485,11 +542,11 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
 #pragma unroll
                         for (int k = 0; k < 2; k++)
                             *reinterpret_cast<float4 *>(dst + 2 * i + 4 * k) =
-                                make_float4(o[t][i][2 * k + j] + cr, o[t][i + 1][2 * k + j] + cr, o[t][i + 2][2 * k + j] + cr,
-                                            o[t][i + 3][2 * k + j] + cr);
+                                make_float4(o[t][i][2 * k + j], o[t][i + 1][2 * k + j], o[t][i + 2][2 * k + j],
+                                            o[t][i + 3][2 * k + j]);
                     if (r == 0)
                         reinterpret_cast<float2 *>(p.ws + 2LL * p.grid * kRows * D)[slot * kRows + row] =
-                            make_float2(top[t][j] == -INFINITY ? -INFINITY : m[t][j] * scale, l[t][j]);
+                            make_float2(m[t][j] == -INFINITY ? -INFINITY : ref[t][j], l[t][j]);
                 }
             }
     }

@@ -3,10 +3,8 @@
 // For a row q (a new token and a query head) and the tokens t it sees,
 //     out = sum_t p_t v_t / sum_t p_t,   p_t = 2^(x_t - m),   x_t = scale log2(e) (q . k_t).
 // With k_t = m_t + s_t c_t and c_t in 0 .. 15,  q . k_t = s_t (q . c_t) + m_t sum(q): the first
-// product runs on the codes, which bf16 holds exactly, and the step and low end come in after it.
-// Likewise sum_t p_t v_t = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (m_t + 8 s_t), where p_t s_t is
-// rounded to bf16 for the second product (its error is that of a bf16 probability) and the rest
-// stays in fp32.  A code becomes a bf16 by one AND-OR: 0x4300 | c is 128 + c.
+// product runs on the codes, which fp16 holds exactly, and the step and low end come in after it.
+// Likewise sum_t p_t v_t = sum_t (p_t s_t) c_t + sum_t p_t m_t.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,8 +38,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// Low nibbles of both halves as two bf16 128 + c.
-__device__ __forceinline__ uint32_t code_pair(uint32_t x) { return (x & 0x000F000Fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

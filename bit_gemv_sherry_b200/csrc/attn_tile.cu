@@ -142,12 +142,6 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t x, uint32_t s, uint32_t 
     return d;
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
-
 // A pair (step, low end) whose values are finite and can be ordered: magnitude bound of its values,
 // 0 where it is not.
 __device__ __forceinline__ float pair_most(uint32_t sm) {

@@ -7,7 +7,9 @@ memory and streams.  There is no CPU fallback: if the library cannot be
 loaded, importing the functions raises.
 """
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -652,58 +654,75 @@ class GroupedCmpGemv:
 
 
 # ----------------------------------------------------------------------------- attention
+# The calls of a decode step are small, so the host side counts: descriptors are packed straight into
+# bytes, and a tensor's properties are read once each (a call takes 6 to 8 us on the host, about half of
+# it the launches; ctypes structures and separate checks took 12 to 22 us).
 KV4_PAGE = 64
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_ROPE = struct.Struct("=QQQQqqqqQQQQqiiiiiiif")   # RopeArgs
+_KV4 = struct.Struct("=QqiiQqqQQqq")              # Kv4Args
+assert _ROPE.size == ctypes.sizeof(RopeArgs) and _KV4.size == ctypes.sizeof(Kv4Args)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 
-def _heads(t, name, dev=None):
-    """(type, rows, heads, D, elements from row to row) of a [T, heads, D] tensor whose
-    rows are contiguous; the row stride is free (a slice of a fused product will do)."""
+def _device(t, name):
+    """Index of the CUDA device of a tensor."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype not in _TYPES:
+    return t.get_device()
+
+
+def _heads(t, name, dev):
+    """(type, rows, heads, D, elements from row to row) of a [T, heads, D] tensor on device `dev` whose
+    rows are contiguous; the row stride is free (a slice of a fused product will do)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise TypeError("%s must be a tensor on CUDA device %d" % (name, dev))
+    ty = _TYPES.get(t.dtype)
+    if ty is None:
         raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
     if t.dim() != 3:
         raise ValueError("%s must have shape [T, heads, D]" % name)
-    if dev is not None and t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
     T, H, D = t.shape
     st, sh, sd = t.stride()
-    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError("%s must have contiguous rows (strides %s)" % (name, t.stride()))
-    return _TYPES[t.dtype], T, H, D, (st if T > 1 else H * D)
+    return ty, T, H, D, (st if T > 1 else H * D)
 
 
 def _index(t, name, dev, dim=1):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != dev:
-        raise TypeError("%s must be an int32 tensor on %s" % (name, dev))
-    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != dev:
+        raise TypeError("%s must be an int32 tensor on CUDA device %d" % (name, dev))
+    if t.dim() != dim or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError("%s must have %d dimension(s), the last contiguous" % (name, dim))
 
 
-def _vector(t, name, dev, n):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != dev:
-        raise TypeError("%s must be a float32 tensor on %s" % (name, dev))
-    if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
-        raise ValueError("%s must be contiguous with %d elements" % (name, n))
+def _vector(t, name, dev, n=None):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.get_device() != dev:
+        raise TypeError("%s must be a float32 tensor on CUDA device %d" % (name, dev))
+    if t.dim() != 1 or (n is not None and t.numel() != n) or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %s elements" % (name, n))
 
 
 def _call(dev, f, where, *args):
-    """f(*args, current stream of dev), with dev the current device."""
-    if dev.index != torch.cuda.current_device():
+    """f(*args, current stream of device dev), with dev the current device."""
+    if _get_device() != dev:
         with torch.cuda.device(dev):
-            _check(f(*args, _stream_handle(dev)), where)
+            st = f(*args, _stream_handle(torch.device("cuda", dev)))
     else:
-        _check(f(*args, _stream_handle(dev)), where)
+        st = f(*args, _raw_stream(dev) if _raw_stream is not None else _stream_handle(torch.device("cuda", dev)))
+    if st:
+        _check(st, where)
 
 
 def _scratch(nbytes, dev):
-    """As workspace(); a call under graph capture gets its own buffer from the graph's pool,
-    so that two graphs that run at the same time share none."""
+    """As workspace(); a call under graph capture gets its own buffer from the graph's pool, so that two
+    graphs that run at the same time share none."""
+    device = torch.device("cuda", dev)
     with torch.cuda.device(dev):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return workspace(nbytes, dev)
+        if _capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace(nbytes, device)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-5,
@@ -714,45 +733,45 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     interleaved.  Returns (q_out, k_out) of out_dtype (default bfloat16); q_out may be q itself."""
     if q is None and k is None:
         raise TypeError("q or k must be given")
-    dev = (q if q is not None else k).device
-    a = RopeArgs()
+    dev = _device(q, "q") if q is not None else _device(k, "k")
+    qp = kp = qop = kop = qs = ks = qos = kos = Hq = Hk = qw = kw = 0
     shape = None
-    for t, out, w, side in ((q, q_out, q_weight, "q"), (k, k_out, k_weight, "k")):
-        if t is None:
-            if out is not None or w is not None:
-                raise TypeError("%s is None but %s_out or %s_weight is given" % (side, side, side))
-            continue
-        ty, T, H, D, stride = _heads(t, side, dev)
-        if out is None:
-            out = torch.empty((T, H, D), dtype=out_dtype or torch.bfloat16, device=dev)
-            if side == "q":
-                q_out = out
-            else:
-                k_out = out
-        oty, oT, oH, oD, ostride = _heads(out, side + "_out", dev)
-        if (oT, oH, oD) != (T, H, D):
-            raise ValueError("%s_out has shape %s, expected %s" % (side, (oT, oH, oD), (T, H, D)))
-        if shape not in (None, (ty, oty, T, D)):
-            raise ValueError("q and k differ in type, tokens or head size")
+    if q is not None:
+        ty, T, Hq, D, qs = _heads(q, "q", dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=out_dtype or torch.bfloat16, device=q.device)
+        oty, oT, oH, oD, qos = _heads(q_out, "q_out", dev)
+        if oT != T or oH != Hq or oD != D:
+            raise ValueError("q_out has shape %s, expected %s" % ((oT, oH, oD), (T, Hq, D)))
+        if q_weight is not None:
+            _vector(q_weight, "q_weight", dev, D)
+            qw = q_weight.data_ptr()
+        qp, qop = q.data_ptr(), q_out.data_ptr()
         shape = (ty, oty, T, D)
-        if w is not None:
-            _vector(w, side + "_weight", dev, D)
-        wp = w.data_ptr() if w is not None else None
-        if side == "q":
-            a.q, a.q_out, a.q_stride, a.q_out_stride, a.q_weight, a.Hq = (
-                t.data_ptr(), out.data_ptr(), stride, ostride, wp, H)
-        else:
-            a.k, a.k_out, a.k_stride, a.k_out_stride, a.k_weight, a.Hk = (
-                t.data_ptr(), out.data_ptr(), stride, ostride, wp, H)
-    ty, oty, T, D = shape
+    elif q_out is not None or q_weight is not None:
+        raise TypeError("q is None but q_out or q_weight is given")
+    if k is not None:
+        ty, T, Hk, D, ks = _heads(k, "k", dev)
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=out_dtype or torch.bfloat16, device=k.device)
+        oty, oT, oH, oD, kos = _heads(k_out, "k_out", dev)
+        if oT != T or oH != Hk or oD != D:
+            raise ValueError("k_out has shape %s, expected %s" % ((oT, oH, oD), (T, Hk, D)))
+        if shape is not None and shape != (ty, oty, T, D):
+            raise ValueError("q and k differ in type, tokens or head size")
+        if k_weight is not None:
+            _vector(k_weight, "k_weight", dev, D)
+            kw = k_weight.data_ptr()
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    elif k_out is not None or k_weight is not None:
+        raise TypeError("k is None but k_out or k_weight is given")
     _index(positions, "positions", dev)
-    if positions.numel() != T:
+    if positions.shape[0] != T:
         raise ValueError("positions has %d entries for %d tokens" % (positions.numel(), T))
-    _vector(inv_freq, "inv_freq", dev, inv_freq.numel())
-    a.positions, a.inv_freq = positions.data_ptr(), inv_freq.data_ptr()
-    a.T, a.D, a.R, a.in_type, a.out_type = T, D, 2 * inv_freq.numel(), ty, oty
-    a.interleaved, a.eps = int(interleaved), eps
-    _call(dev, lib().sherry_qk_norm_rope, "sherry_qk_norm_rope", ctypes.addressof(a))
+    _vector(inv_freq, "inv_freq", dev)
+    args = _ROPE.pack(qp, kp, qop, kop, qs, ks, qos, kos, positions.data_ptr(), inv_freq.data_ptr(), qw, kw, T,
+                      Hq, Hk, D, 2 * inv_freq.shape[0], ty, oty, 1 if interleaved else 0, eps)
+    _call(dev, lib().sherry_qk_norm_rope, "sherry_qk_norm_rope", args)
     return q_out, k_out
 
 
@@ -764,50 +783,53 @@ def kv4_cache(pages, heads, dim, device):
     return torch.zeros((pages, heads, 2, KV4_PAGE * (dim // 2 + 4)), dtype=torch.uint8, device=device)
 
 
-def _kv4(cache, page_table, ctx_lens, cu_q, T):
-    if not isinstance(cache, torch.Tensor) or not cache.is_cuda or cache.dtype != torch.uint8:
+_BLOCK_DIM = {KV4_PAGE * (d // 2 + 4): d for d in (64, 128)}
+
+
+def _kv4(cache, page_table, ctx_lens, cu_q, T, dev):
+    """(Kv4Args as bytes, heads, D)."""
+    if cache.dtype is not torch.uint8:
         raise TypeError("cache must be a uint8 CUDA tensor (kv4_cache)")
     if cache.dim() != 4 or cache.shape[2] != 2 or not cache.is_contiguous():
         raise ValueError("cache must be contiguous, [pages, heads, 2, 64 * (dim / 2 + 4)]")
-    dev = cache.device
     pages, H, _, block = cache.shape
-    D = (block // KV4_PAGE - 4) * 2
-    if D not in (64, 128) or block != KV4_PAGE * (D // 2 + 4):
+    D = _BLOCK_DIM.get(block)
+    if D is None:
         raise ValueError("cache blocks of %d bytes are of no head size" % block)
     _index(page_table, "page_table", dev, 2)
     _index(ctx_lens, "ctx_lens", dev)
     B, width = page_table.shape
-    if ctx_lens.numel() != B:
+    if ctx_lens.shape[0] != B:
         raise ValueError("ctx_lens has %d entries, page_table %d rows" % (ctx_lens.numel(), B))
+    cu = 0
     if cu_q is not None:
         _index(cu_q, "cu_q", dev)
-        if cu_q.numel() != B + 1:
+        if cu_q.shape[0] != B + 1:
             raise ValueError("cu_q has %d entries for %d sequences" % (cu_q.numel(), B))
+        cu = cu_q.data_ptr()
     elif T != B:
         raise ValueError("%d rows for %d sequences: give cu_q" % (T, B))
-    return Kv4Args(cache.data_ptr(), pages, H, D, page_table.data_ptr(), width,
-                   page_table.stride(0) if B > 1 else width, ctx_lens.data_ptr(),
-                   cu_q.data_ptr() if cu_q is not None else None, B, T), dev
+    return _KV4.pack(cache.data_ptr(), pages, H, D, page_table.data_ptr(), width,
+                     page_table.stride(0) if B > 1 else width, ctx_lens.data_ptr(), cu, B, T), H, D
 
 
-def _kv4_pair(k, v, cache):
-    ty, T, H, D, ks = _heads(k, "k", cache.device)
-    vty, vT, vH, vD, vs = _heads(v, "v", cache.device)
-    if (ty, T, H, D) != (vty, vT, vH, vD):
+def _kv4_rows(f, where, cache, k, v, page_table, ctx_lens, cu_q):
+    dev = _device(cache, "cache")
+    ty, T, H, D, ks = _heads(k, "k", dev)
+    vty, vT, vH, vD, vs = _heads(v, "v", dev)
+    if vty != ty or vT != T or vH != H or vD != D:
         raise ValueError("k and v differ in type or shape")
-    return ty, T, H, D, ks, vs
+    args, cH, cD = _kv4(cache, page_table, ctx_lens, cu_q, T, dev)
+    if H != cH or D != cD:
+        raise ValueError("k has %d heads of %d, the cache %d of %d" % (H, D, cH, cD))
+    _call(dev, f, where, args, k.data_ptr(), v.data_ptr(), ty, ks, vs)
 
 
 def kv4_write(cache, k, v, page_table, ctx_lens, cu_q=None):
     """Codes the new tokens' k and v [T, heads, dim] (fp32 or bf16) into the cache.  page_table int32
     [B, width], ctx_lens int32 [B] (the new tokens included); rows cu_q[b] .. cu_q[b + 1] - 1 are the
     last positions of sequence b (cu_q None: one row each)."""
-    ty, T, H, D, ks, vs = _kv4_pair(k, v, cache)
-    a, dev = _kv4(cache, page_table, ctx_lens, cu_q, T)
-    if (H, D) != (a.H, a.D):
-        raise ValueError("k has %d heads of %d, the cache %d of %d" % (H, D, a.H, a.D))
-    _call(dev, lib().sherry_kv4_write, "sherry_kv4_write", ctypes.addressof(a), k.data_ptr(), v.data_ptr(),
-          ty, ks, vs)
+    _kv4_rows(lib().sherry_kv4_write, "sherry_kv4_write", cache, k, v, page_table, ctx_lens, cu_q)
 
 
 def kv4_read(cache, page_table, ctx_lens, cu_q=None, rows=None, dtype=torch.float32, k=None, v=None):
@@ -821,18 +843,15 @@ def kv4_read(cache, page_table, ctx_lens, cu_q=None, rows=None, dtype=torch.floa
             if cu_q is not None:
                 raise TypeError("rows must be given with cu_q")
             rows = ctx_lens.numel()
-        a, dev = _kv4(cache, page_table, ctx_lens, cu_q, rows)
-        k = torch.zeros((rows, a.H, a.D), dtype=dtype, device=dev)
-        v = torch.zeros((rows, a.H, a.D), dtype=dtype, device=dev)
-    ty, T, H, D, ks, vs = _kv4_pair(k, v, cache)
-    a, dev = _kv4(cache, page_table, ctx_lens, cu_q, T)
-    if (H, D) != (a.H, a.D):
-        raise ValueError("k has %d heads of %d, the cache %d of %d" % (H, D, a.H, a.D))
-    _call(dev, lib().sherry_kv4_read, "sherry_kv4_read", ctypes.addressof(a), k.data_ptr(), v.data_ptr(),
-          ty, ks, vs)
+        dev = _device(cache, "cache")
+        _, H, D = _kv4(cache, page_table, ctx_lens, cu_q, rows, dev)
+        k = torch.zeros((rows, H, D), dtype=dtype, device=cache.device)
+        v = torch.zeros((rows, H, D), dtype=dtype, device=cache.device)
+    _kv4_rows(lib().sherry_kv4_read, "sherry_kv4_read", cache, k, v, page_table, ctx_lens, cu_q)
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_kv4_workspace_bytes(T, heads, dim):
     return int(lib().sherry_attn_kv4_workspace_bytes(T, heads, dim))
 
@@ -842,22 +861,27 @@ def attn_kv4(q, cache, page_table, ctx_lens, cu_q=None, max_q=0, scale=None, out
     written before): out bf16 [T, Hq, dim].  page_table, ctx_lens and cu_q as for kv4_write; scale
     defaults to dim ** -0.5; max_q, the most new tokens of a sequence, helps to pick kernels (0: not
     known).  Rows without a position give zeros."""
-    ty, T, Hq, D, qs = _heads(q, "q", cache.device)
-    a, dev = _kv4(cache, page_table, ctx_lens, cu_q, T)
+    dev = _device(cache, "cache")
+    ty, T, Hq, D, qs = _heads(q, "q", dev)
+    args, H, cD = _kv4(cache, page_table, ctx_lens, cu_q, T, dev)
     if out is None:
         make = torch.empty if cu_q is None else torch.zeros  # rows outside every sequence stay
-        out = make((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = make((T, Hq, D), dtype=torch.bfloat16, device=q.device)
     oty, oT, oH, oD, os_ = _heads(out, "out", dev)
     if ty != 1 or oty != 1:
         raise TypeError("q and out must be bfloat16")
-    if (oT, oH, oD) != (T, Hq, D):
+    if oT != T or oH != Hq or oD != D:
         raise ValueError("out has shape %s, expected %s" % ((oT, oH, oD), (T, Hq, D)))
-    if D != a.D or Hq % a.H:
-        raise ValueError("q has %d heads of %d, the cache %d of %d" % (Hq, D, a.H, a.D))
+    if D != cD or Hq % H:
+        raise ValueError("q has %d heads of %d, the cache %d of %d" % (Hq, D, H, cD))
     if ws is None:
-        ws = _scratch(attn_kv4_workspace_bytes(T, Hq, D), dev)
-    _call(dev, lib().sherry_attn_kv4, "sherry_attn_kv4", ctypes.addressof(a), q.data_ptr(), qs,
-          out.data_ptr(), os_, Hq, int(max_q), D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
+        need = attn_kv4_workspace_bytes(T, Hq, D)
+        if _raw_stream is not None and _get_device() == dev and not _capturing():
+            ws = _workspaces.get((dev, _raw_stream(dev)))
+        if ws is None or ws.numel() < need:
+            ws = _scratch(need, dev)
+    _call(dev, lib().sherry_attn_kv4, "sherry_attn_kv4", args, q.data_ptr(), qs, out.data_ptr(), os_, Hq, int(max_q),
+          D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
     return out
 
 

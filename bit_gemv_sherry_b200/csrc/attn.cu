@@ -13,7 +13,7 @@ namespace {
 // The bytes of the cache are the bound: 2 (D / 2 + 4) per token and head.  The work is the pages of the
 // batch in the order (sequence, head, row tile, page), a row tile being up to 8 NT rows (query heads that
 // share a key/value head, times new tokens).  It is cut into equal runs, one per warp, so that long and
-// short sequences load the machine alike; row tiles that a run does not hold whole go to the workspace
+// short sequences load the machine alike (and as few runs as that takes: fewer parts to join); row tiles that a run does not hold whole go to the workspace
 // and a second kernel joins their parts in the order of the runs (no atomics: results do not depend on
 // timing).  A warp works alone: it copies its pages into its own ring (a page's keys and values are one
 // contiguous block: one bulk copy), and no other warp waits for it.
@@ -66,8 +66,14 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams &p, int b) {
 // The batch's work as this launch divides it.
 struct Work {
     long long total;  // work of all row tiles: pages, and `cost` for each row tile
-    int cost, runs;
+    long long each;   // a run's share: run i takes places [i each, (i + 1) each)
+    int cost;
 };
+
+// a / b for a >= 0, b > 0, mostly small.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 template <int ROWS>
 __device__ Work all_work(const AttnParams &p) {
@@ -85,7 +91,7 @@ __device__ Work all_work(const AttnParams &p) {
     Work w;
     w.cost = pages >= 4LL * p.grid ? kUnitCost : 0;
     w.total = pages + units * w.cost;
-    w.runs = (int)min((long long)p.grid, w.total);
+    w.each = quotient(w.total + p.grid - 1, p.grid);
     return w;
 }
 
@@ -120,10 +126,6 @@ __device__ void find_seq(const AttnParams &p, const Work &w, long long x, int &b
     before = base;
 }
 
-// Run i takes places [i T / n, (i + 1) T / n) of the work; place x lies in run ((x + 1) n - 1) / T.
-__device__ __forceinline__ long long run_start(const Work &w, int i) { return w.total * i / w.runs; }
-__device__ __forceinline__ int run_of(const Work &w, long long x) { return (int)(((x + 1) * w.runs - 1) / w.total); }
-
 // A walk over a run, one piece (pages of one (sequence, head, row tile)) at a time.
 template <int ROWS>
 struct Walk {
@@ -148,7 +150,7 @@ struct Walk {
                 if (++b >= p.c.B) return false;
                 s = seq_work<ROWS>(p, b);
             }
-            const int unit = (int)((x - before) / (s.pages + cost));
+            const int unit = (int)quotient(x - before, s.pages + cost);
             const long long at = before + (long long)unit * (s.pages + cost);  // the row tile's first place
             page0 = max((int)(x - at) - cost, 0);
             page1 = (int)min((long long)s.pages, end - at - cost);
@@ -205,12 +207,12 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
     asm volatile("griddepcontrol.wait;" ::: "memory");  // lengths and cache come from the kernels before
     const Work work = all_work<kRows>(p);
     const int run = blockIdx.x + gridDim.x * warp;      // neighbouring runs on different SMs
-    if (run >= work.runs) return;
-    const long long from = run_start(work, run), to = run_start(work, run + 1);
+    const long long from = run * work.each, to = min(from + work.each, work.total);
+    if (from >= to) return;
     Walk<kRows> walk;
     walk.start(p, work, from, to);
 
-    int copied = 0;
+    int copied = 0, to_copy = 0;
     if (lane == 0) {
         ahead = walk;
         ahead.page1 = ahead_page = 0;
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             ahead_page = ahead.page0;
             if (ahead.s.len > p.c.width * SHERRY_KV4_PAGE) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
         }
-        const int s = copied % kS;
+        const int s = to_copy;
         const int page = ahead.s.len > 0 ? kv4_page(p.c, ahead.b, ahead_page * SHERRY_KV4_PAGE, p.err) : -1;
         there[s] = page >= 0;
         if (page >= 0) {
@@ -232,6 +234,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
         }
         ahead_page++;
         copied++;
+        to_copy = to_copy + 1 == kS ? 0 : to_copy + 1;
     };
     if (lane == 0)
         for (int s = 0; s < kS; s++) copy_next();
@@ -243,7 +246,8 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
     const int tok_r = r ^ (r >> 2 & 1);                       // rows r and r + 8 (+ 8)
     const int tok_v0 = (2 * c) ^ (c >> 1 & 1), tok_v1 = (2 * c + 1) ^ (c >> 1 & 1);
     const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;  // a negative scale turns q's signs
-    uint32_t it = 0;
+    int it = 0, s = 0;        // pages done, ring slot of the next
+    uint32_t lap = 0;         // its phase
     bool dead = false;
     while (walk.next(p)) {
         const int nrow = walk.s.rows * p.g, row0 = walk.tile * kRows;
@@ -296,7 +300,8 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 qsum[t][j] = __shfl_sync(0xFFFFFFFFu, sum, (2 * c + j) * 4);
-                sc[t][j] = fabsf(p.scale2) * pow2(24 + __shfl_sync(0xFFFFFFFFu, e, (2 * c + j) * 4));
+                // (not 0: a score of -inf has to stay one)
+                sc[t][j] = fmaxf(fabsf(p.scale2) * pow2(24 + __shfl_sync(0xFFFFFFFFu, e, (2 * c + j) * 4)), 1e-37f);
                 const int rw = row0 + 8 * t + 2 * c + j;
                 last[t][j] = rw < nrow ? pos0 + rw / p.g : -1;
             }
@@ -320,8 +325,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             for (int j = 0; j < 2; j++) m[t][j] = -INFINITY, ref[t][j] = 0.0f, l[t][j] = 0.0f, corr[t][j] = 0.0f;
         }
         for (int pg = walk.page0; pg < walk.page1; pg++, it++) {
-            const int s = it % kS;
-            dead = dead || !__all_sync(0xFFFFFFFFu, mbar_wait(full + s, (it / kS) & 1, abort, p.err, p.wait_limit));
+            dead = dead || !__all_sync(0xFFFFFFFFu, mbar_wait(full + s, lap, abort, p.err, p.wait_limit));
             const int t0 = pg * SHERRY_KV4_PAGE;              // first token of the page
             if (!dead && there[s] && t0 <= last_max) {
                 const uint8_t *kb = ring + s * F::kStage, *vb = kb + Kv4<D>::kBlock;
@@ -377,18 +381,22 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                         mv[qi][i] = kv4_low(vp);
                     }
                 if (!whole) {
-                    // a token that a row does not see may hold anything, NaN too
+                    // A token that a row does not see may hold anything: its probability is 2^-inf, and a step or
+                    // low end that is not a number goes to the score of the rows that do see it.
 #pragma unroll
                     for (int qi = 0; qi < kTiles; qi++)
 #pragma unroll
                         for (int i = 0; i < 2; i++) {
                             const int tok = t0 + 16 * (q0 + qi) + tok_r + 8 * i;
-                            if (tok > last_max) sv[qi][i] = mv[qi][i] = 0.0f;
+                            const bool bad = !(fabsf(sv[qi][i]) < INFINITY && fabsf(mv[qi][i]) < INFINITY);
+                            if (bad || tok > last_max) sv[qi][i] = mv[qi][i] = 0.0f;
 #pragma unroll
                             for (int t = 0; t < NT; t++)
 #pragma unroll
-                                for (int j = 0; j < 2; j++)
+                                for (int j = 0; j < 2; j++) {
+                                    if (bad) x[qi][t][2 * i + j] = __int_as_float(0x7FFFFFFF);
                                     if (tok > last[t][j]) x[qi][t][2 * i + j] = -INFINITY;
+                                }
                         }
                 }
                 float step = fmaxf(sv[0][0], sv[0][1]);
@@ -413,12 +421,10 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                                 float ps[2];
 #pragma unroll
                                 for (int j = 0; j < 2; j++) {
-                                    float pr = exp2_fast(x[qi][t][2 * i + j] * sc[t][j] - ref[t][j]);
-                                    float pm = pr * mv[qi][i];
+                                    const float pr = exp2_fast(x[qi][t][2 * i + j] * sc[t][j] - ref[t][j]);
                                     ps[j] = pr * sv[qi][i];
-                                    if (!whole && x[qi][t][2 * i + j] == -INFINITY) pr = pm = ps[j] = 0.0f;
                                     sum[t][j] += pr;
-                                    csum[t][j] += pm;
+                                    csum[t][j] += pr * mv[qi][i];
                                 }
                                 pb[qi][t][i] = pack_f16(ps[0], ps[1]);
                             }
@@ -495,6 +501,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             }
             __syncwarp();
             if (lane == 0 && !dead) copy_next();
+            if (++s == kS) s = 0, lap ^= 1;
         }
 
         // ---------------- the piece's result ----------------
@@ -553,19 +560,20 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
     if (dead && lane == 0) {
         // copies in flight land before the CTA's shared memory is released
         volatile int no_abort = 0;
-        for (int j = max((int)it, copied - kS); j < copied; j++)
+        for (int j = max(it, copied - kS); j < copied; j++)
             mbar_wait(full + j % kS, (j / kS) & 1, &no_abort, p.err, 1000000000LL);
     }
 }
 
-// Joins the parts of the row tiles that the runs cut: a CTA per row tile, a warp per row, the parts in the
-// order of the runs.
-template <int D, int NT>
-__global__ void __launch_bounds__(256 * NT, 2) attn_join_kernel(const __grid_constant__ AttnParams p) {
+// Joins the parts of the row tiles that the runs cut: a CTA per 8 rows of one, JW warps per row, which take
+// 32 parts in turn and whose sums are added in order.
+template <int D, int NT, int JW>
+__global__ void __launch_bounds__(256 * JW, JW == 1 ? 2 : 1) attn_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kRows = 8 * NT, E = D / 32;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int mine = warp % JW, row = warp / JW + 8 * blockIdx.y;
     const Work work = all_work<kRows>(p);
     int b;
     long long units, before;
@@ -581,19 +589,20 @@ __global__ void __launch_bounds__(256 * NT, 2) attn_join_kernel(const __grid_con
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     const int h = unit / s.tiles, rw = (unit - h * s.tiles) * kRows + row;
-    if (rw >= s.rows * p.g) return;
     const long long x0 = before + (long long)unit * (s.pages + work.cost) + work.cost;  // the first page's place
-    const int i0 = run_of(work, x0), i1 = run_of(work, x0 + s.pages - 1);
+    const int i0 = (int)quotient(x0, work.each), i1 = (int)quotient(x0 + s.pages - 1, work.each);
     if (i0 == i1) return;  // one run held all of it and wrote the result
+    const bool live = rw < s.rows * p.g;
+    if (JW == 1 && !live) return;
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws + 2LL * p.grid * kRows * D);
     float m = -INFINITY;
-    for (int i = i0 + lane; i <= i1; i += 32) m = fmaxf(m, ml[(2LL * i + (i == i0)) * kRows + row].x);
+    for (int i = i0 + lane; live && i <= i1; i += 32) m = fmaxf(m, ml[(2LL * i + (i == i0)) * kRows + row].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     float l = 0.0f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; e++) acc[e] = 0.0f;
-    for (int ib = i0; ib <= i1; ib += 32) {
+    for (int ib = i0 + 32 * mine; live && ib <= i1; ib += 32 * JW) {
         const int i = ib + lane;
         float f = 0.0f;
         if (i <= i1) {
@@ -619,6 +628,22 @@ __global__ void __launch_bounds__(256 * NT, 2) attn_join_kernel(const __grid_con
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    if (JW > 1) {
+        __shared__ float part[8][JW][D + 1];
+        float *to = part[warp / JW][mine];
+#pragma unroll
+        for (int e = 0; e < E; e++) to[lane * E + e] = acc[e];
+        if (lane == 0) to[D] = l;
+        __syncthreads();
+        if (!live || mine != 0) return;
+#pragma unroll
+        for (int w = 1; w < JW; w++) {
+            const float *from = part[warp / JW][w];
+            l += from[D];
+#pragma unroll
+            for (int e = 0; e < E; e++) acc[e] += from[lane * E + e];
+        }
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint16_t *dst = p.out + (long long)(s.first + rw / p.g) * p.out_stride + (long long)(h * p.g + rw % p.g) * D + lane * E;
 #pragma unroll
@@ -676,7 +701,11 @@ sherry_status few_launch(AttnParams p, cudaStream_t stream) {
     if (!p.c.cu) tiles = (long long)p.c.B * ((p.g + F::kRows - 1) / F::kRows);
     tiles *= p.c.H;
     if (tiles > 0x7FFFFFFF) return SHERRY_ERR_UNSUPPORTED;
-    launch_after(attn_join_kernel<D, NT>, dim3((unsigned)tiles), 256 * NT, 0, stream, p);
+    // Up to about this many parts a row tile: four warps a row for one long sequence (24 us against 36 at
+    // 32,768 tokens, heads of 64), one for many (29 us against 41 for 64 sequences of 1,024).
+    const long long parts = std::min<long long>(p.grid / tiles, p.c.width);
+    if (parts > 32) launch_after(attn_join_kernel<D, NT, 4>, dim3((unsigned)tiles, NT), 1024, 0, stream, p);
+    else launch_after(attn_join_kernel<D, NT, 1>, dim3((unsigned)tiles, NT), 256, 0, stream, p);
     return launch_status("sherry_attn_kv4 (join)");
 }
 

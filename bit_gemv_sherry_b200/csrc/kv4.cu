@@ -11,6 +11,7 @@ __device__ unsigned int g_kv4_device_error = 0;
 namespace {
 
 constexpr int kKvThreads = 256;
+constexpr long long kManySteps = 148 * 64 * 4;  // warp steps of a few waves
 
 struct KvIo {
     void *k, *v;
@@ -29,110 +30,184 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return d;
 }
 
-// Eight consecutive elements as fp32.
+// Eight consecutive elements as they are in memory, and as fp32.
 template <bool BF>
-__device__ __forceinline__ void load8(const void *base, long long at, float (&x)[8]) {
+__device__ __forceinline__ void load8(const void *base, long long at, uint4 (&u)[BF ? 1 : 2]) {
     if (BF) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        u[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
+    } else {
+        const uint4 *f = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
+        u[0] = f[0];
+        u[BF ? 0 : 1] = f[1];
+    }
+}
+template <bool BF>
+__device__ __forceinline__ void floats8(const uint4 (&u)[BF ? 1 : 2], float (&x)[8]) {
+    if (BF) {
+        const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             x[2 * i] = __uint_as_float(w[i] << 16);
             x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     } else {
-        const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
-        const float4 a = f[0], b = f[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const uint4 v = u[BF ? 0 : i];
+            x[4 * i] = __uint_as_float(v.x), x[4 * i + 1] = __uint_as_float(v.y);
+            x[4 * i + 2] = __uint_as_float(v.z), x[4 * i + 3] = __uint_as_float(v.w);
+        }
     }
 }
 
-// A row of D elements is D / 8 lanes of eight elements, one code word each.  A
-// thread's row index runs over (row, head, K or V): neighbouring lanes read
-// neighbouring memory of the tensors.
-template <int D, bool BF, bool WRITE>
-__global__ void __launch_bounds__(kKvThreads)
-    kv4_rows_kernel(const __grid_constant__ Kv4View c, const __grid_constant__ KvIo io, unsigned int *err) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int L = D / 8;
-    const int sub = threadIdx.x & (L - 1);
-    const long long i = ((long long)blockIdx.x * kKvThreads + threadIdx.x) / L;
-    const int per = 2 * c.H;
-    const long long t = i / per;
-    const int rest = (int)(i - t * per);
-    const int kv = rest >= c.H ? 1 : 0, h = rest - kv * c.H;
-    int b = 0, pos = -1, page = -1;
-    if (t < c.T && kv4_find(c, (int)t, b, pos) && pos >= 0) page = kv4_page(c, b, pos, err);
-    // a row's lanes share t, h and kv, so they leave together; the shuffles below
-    // name only the row's lanes
-    if (page < 0) return;
-    const int slot = pos % SHERRY_KV4_PAGE;
-    uint8_t *blk = kv4_block<D>(c, page, h, kv);
-    uint32_t *code = reinterpret_cast<uint32_t *>(blk + slot * Kv4<D>::kRow) + sub;
-    uint32_t *sm = reinterpret_cast<uint32_t *>(blk + Kv4<D>::kCodes) + slot;
-    void *base = kv ? io.v : io.k;
-    const long long at = t * (kv ? io.v_stride : io.k_stride) + (long long)h * D + 8 * sub;
-    if (WRITE) {
-        float x[8];
-        load8<BF>(base, at, x);
-        float lo = x[0], hi = x[0];
+// min and max of two bf16 pairs, keeping a NaN
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Smallest and largest element of a row of L lanes.  bf16: both in one register, (min, -max), so that one
+// shuffle a level serves both.
+template <bool BF, int L>
+__device__ __forceinline__ void row_range(const uint4 (&u)[BF ? 1 : 2], const float (&x)[8], float &lo, float &hi) {
+    if (BF) {
+        const uint32_t neg = 0x80008000u;
+        const uint32_t a = min2_nan(min2_nan(u[0].x, u[0].y), min2_nan(u[0].z, u[0].w));
+        const uint32_t b = min2_nan(min2_nan(u[0].x ^ neg, u[0].y ^ neg), min2_nan(u[0].z ^ neg, u[0].w ^ neg));
+        // (a.lo, b.lo) and (a.hi, b.hi)
+        uint32_t m = min2_nan(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = min2_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        lo = __uint_as_float(m << 16);
+        hi = -__uint_as_float(m & 0xFFFF0000u);
+    } else {
+        lo = x[0], hi = x[0];
 #pragma unroll
         for (int j = 1; j < 8; j++) {
             lo = min_nan(lo, x[j]);
             hi = max_nan(hi, x[j]);
         }
-        const uint32_t mask = (L == 32 ? 0xFFFFFFFFu : ((1u << L) - 1u)) << ((threadIdx.x & 31) & ~(L - 1));
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(mask, lo, o));
-            hi = max_nan(hi, __shfl_xor_sync(mask, hi, o));
-        }
-        const uint32_t s16 = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f)));
-        const uint32_t m16 = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-        uint32_t pair = s16 | (m16 << 16);
-        const float s = kv4_step(pair), m = kv4_low(pair);
-        uint32_t word = 0;
-        if (!(isfinite(s) && isfinite(m))) {
-            pair = 0x7FFF7FFFu;  // NaN, NaN
-        } else if (s < 7.52316384526264e-37f) {  // 2^-120: 1 / s would overflow soon after
-            pair &= 0xFFFF0000u;
-        } else {
-            const float inv = __frcp_rn(s);
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const float q = rintf(__fmul_rn(__fsub_rn(x[j], m), inv));
-                word |= (uint32_t)fminf(fmaxf(q, 0.0f), 15.0f) << (4 * j);
-            }
-        }
-        *code = word;
-        if (sub == 0) *sm = pair;
-    } else {
-        const uint32_t word = *code, pair = *sm;
-        const float s = kv4_step(pair), m = kv4_low(pair);
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) x[j] = __fmaf_rn(s, (float)((word >> (4 * j)) & 15u), m);
-        if (BF) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-                w[j] = *reinterpret_cast<const uint32_t *>(&v);
-            }
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
-            f[0] = make_float4(x[0], x[1], x[2], x[3]);
-            f[1] = make_float4(x[4], x[5], x[6], x[7]);
+            lo = min_nan(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
         }
     }
 }
 
-template <int D, bool BF, bool WRITE>
-void rows_launch(const Kv4View &c, const KvIo &io, unsigned int *err, cudaStream_t stream) {
-    const long long threads = (long long)c.T * 2 * c.H * (D / 8);
+// A row of D elements is D / 8 lanes of eight elements, one code word each.  A warp takes up to STEPS
+// times 32 lanes' worth of one token's rows (the key heads, then the value heads): the token's page is
+// looked up once, and all of the warp's loads are under way before the first is used.  One read and one
+// write per element bound it, if the conversions keep to the fast pipes: a code becomes a float, and a
+// float a code, by adding 2^23 or 1.5 2^23 (the conversion instructions run at a quarter of the rate:
+// 32,768 tokens with heads of 128 took 84 us to write and 63 to read with them).
+template <int D, int STEPS>
+__host__ __device__ constexpr int rows_per_warp() { return STEPS * 32 / (D / 8); }
+
+template <int D, bool BF, bool WRITE, int STEPS>
+__global__ void __launch_bounds__(kKvThreads)
+    kv4_rows_kernel(const __grid_constant__ Kv4View c, const __grid_constant__ KvIo io, unsigned int *err) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int L = D / 8, kRows = rows_per_warp<D, STEPS>();
+    const int lane = threadIdx.x & 31, sub = lane & (L - 1);
+    const unsigned parts = (unsigned)(2 * c.H + kRows - 1) / kRows;
+    const unsigned w = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
+    const int t = (int)(w / parts), row0 = (int)(w % parts) * kRows + lane / L;
+    if (t >= c.T) return;
+    // row r: head r of the keys, or head r - H of the values
+    const long long k_at = t * io.k_stride + 8 * sub, v_at = t * io.v_stride - (long long)c.H * D + 8 * sub;
+    auto at = [&](int r) { return (r < c.H ? k_at : v_at) + (long long)r * D; };
+    uint4 u[STEPS][BF ? 1 : 2];
+    if (WRITE) {
+#pragma unroll
+        for (int i = 0; i < STEPS; i++) {
+            const int r = row0 + i * (32 / L);
+            if (r < 2 * c.H) load8<BF>(r < c.H ? io.k : io.v, at(r), u[i]);
+        }
+    }
+    int b = 0, pos = -1, page = -1;
+    if (kv4_find(c, t, b, pos) && pos >= 0) page = kv4_page(c, b, pos, err);
+    if (page < 0) return;
+    const int slot = pos % SHERRY_KV4_PAGE;
+    uint8_t *first = kv4_block<D>(c, page, 0, 0);
+    auto block = [&](int r) { return first + (long long)(r < c.H ? 2 * r : 2 * (r - c.H) + 1) * Kv4<D>::kBlock; };
+    if (WRITE) {
+#pragma unroll
+        for (int i = 0; i < STEPS; i++) {
+            const int r = row0 + i * (32 / L);
+            const bool in = r < 2 * c.H;
+            float x[8], lo, hi;
+            floats8<BF>(u[i], x);
+            row_range<BF, L>(u[i], x, lo, hi);  // (lanes past the last row take part with whatever they hold)
+            const uint32_t s16 = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f)));
+            const uint32_t m16 = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
+            uint32_t pair = s16 | (m16 << 16);
+            const float s = kv4_step(pair), m = kv4_low(pair);
+            const bool bad = !(fabsf(s) < INFINITY && fabsf(m) < INFINITY);
+            const bool flat = s < 7.52316384526264e-37f;  // 2^-120: 1 / s would overflow soon after
+            uint32_t word = 0;
+            if (!bad && !flat) {
+                const float inv = __frcp_rn(s);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    // clamped first: the bounds are whole numbers, so the rounding commutes with them
+                    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[j], m), inv), 0.0f), 15.0f);
+                    word += __float_as_uint(__fadd_rn(q, 12582912.0f)) << (4 * j);  // 0x4B400000 + rint(q)
+                }
+                word -= 0x3F400000u;  // what is left of the eight constants: 0x4B400000 (1 + 16 + 256) modulo 2^32
+            }
+            if (bad) pair = 0x7FFF7FFFu;        // NaN, NaN
+            else if (flat) pair &= 0xFFFF0000u;
+            if (in) {
+                uint8_t *blk = block(r);
+                reinterpret_cast<uint32_t *>(blk + slot * Kv4<D>::kRow)[sub] = word;
+                if (sub == 0) reinterpret_cast<uint32_t *>(blk + Kv4<D>::kCodes)[slot] = pair;
+            }
+        }
+    } else {
+        uint32_t word[STEPS], pair[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; i++) {
+            const int r = row0 + i * (32 / L);
+            if (r >= 2 * c.H) continue;
+            const uint8_t *blk = block(r);
+            word[i] = reinterpret_cast<const uint32_t *>(blk + slot * Kv4<D>::kRow)[sub];
+            pair[i] = reinterpret_cast<const uint32_t *>(blk + Kv4<D>::kCodes)[slot];
+        }
+#pragma unroll
+        for (int i = 0; i < STEPS; i++) {
+            const int r = row0 + i * (32 / L);
+            if (r >= 2 * c.H) continue;
+            const float s = kv4_step(pair[i]), m = kv4_low(pair[i]);
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float code = __uint_as_float(((word[i] >> (4 * j)) & 15u) | 0x4B000000u) - 8388608.0f;  // exact
+                x[j] = __fmaf_rn(s, code, m);
+            }
+            void *base = r < c.H ? io.k : io.v;
+            if (BF) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                    w[j] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at(r)) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(base) + at(r));
+                f[0] = make_float4(x[0], x[1], x[2], x[3]);
+                f[1] = make_float4(x[4], x[5], x[6], x[7]);
+            }
+        }
+    }
+}
+
+template <int D, bool BF, bool WRITE, int STEPS>
+void rows_launch_steps(const Kv4View &c, const KvIo &io, unsigned int *err, cudaStream_t stream) {
+    const long long threads = 32LL * c.T * ((2 * c.H + rows_per_warp<D, STEPS>() - 1) / rows_per_warp<D, STEPS>());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((threads + kKvThreads - 1) / kKvThreads));
     cfg.blockDim = dim3(kKvThreads);
@@ -142,7 +217,14 @@ void rows_launch(const Kv4View &c, const KvIo &io, unsigned int *err, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kv4_rows_kernel<D, BF, WRITE>, c, io, err);
+    cudaLaunchKernelEx(&cfg, kv4_rows_kernel<D, BF, WRITE, STEPS>, c, io, err);
+}
+
+template <int D, bool BF, bool WRITE>
+void rows_launch(const Kv4View &c, const KvIo &io, unsigned int *err, cudaStream_t stream) {
+    // Few rows: one step per warp, for the latency; many: four, for the loads under way.
+    if ((long long)c.T * 2 * c.H * (D / 8) / 32 < kManySteps) rows_launch_steps<D, BF, WRITE, 1>(c, io, err, stream);
+    else rows_launch_steps<D, BF, WRITE, 4>(c, io, err, stream);
 }
 
 template <bool WRITE>
@@ -155,7 +237,7 @@ sherry_status rows_call(const sherry_kv4 *c, void *k, void *v, int type, int64_t
     if (k_stride < (int64_t)c->H * c->D || v_stride < (int64_t)c->H * c->D) return SHERRY_ERR_SHAPE;
     const int unit = type == SHERRY_F32 ? 4 : 8;
     if (!aligned(k, 16) || !aligned(v, 16) || k_stride % unit || v_stride % unit) return SHERRY_ERR_ALIGN;
-    if (c->T * 2 * c->H * (c->D / 8) / kKvThreads >= 0x7FFFFFFF) return SHERRY_ERR_UNSUPPORTED;
+    if (c->T * 2 * c->H >= 0x7FFFFFFF) return SHERRY_ERR_UNSUPPORTED;
     const Kv4View view = kv4_view(c);
     const KvIo io = {k, v, k_stride, v_stride};
     unsigned int *err = kv4_error_address();

@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kKvThreads)
     if (page < 0) return;
     const int slot = pos % SHERRY_KV4_PAGE;
     uint8_t *first = kv4_block<D>(c, page, 0, 0);
-    auto block = [&](int r) { return first + (long long)(r < c.H ? 2 * r : 2 * (r - c.H) + 1) * Kv4<D>::kBlock; };
+    // (below 2^31 for 65,535 heads)
+    auto block = [&](int r) { return first + (unsigned)(r < c.H ? 2 * r : 2 * (r - c.H) + 1) * (unsigned)Kv4<D>::kBlock; };
     if (WRITE) {
 #pragma unroll
         for (int i = 0; i < STEPS; i++) {
@@ -150,11 +151,22 @@ __global__ void __launch_bounds__(kKvThreads)
             uint32_t word = 0;
             if (!bad && !flat) {
                 const float inv = __frcp_rn(s);
+                // Every operation is monotone, so the row's ends tell whether any code needs clamping.
+                if (__fmul_rn(__fsub_rn(lo, m), inv) >= -0.5f && __fmul_rn(__fsub_rn(hi, m), inv) < 15.5f) {
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    // clamped first: the bounds are whole numbers, so the rounding commutes with them
-                    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[j], m), inv), 0.0f), 15.0f);
-                    word += __float_as_uint(__fadd_rn(q, 12582912.0f)) << (4 * j);  // 0x4B400000 + rint(q)
+                    for (int j = 0; j < 8; j += 2) {
+                        float a, b;  // 0x4B400000 + rint (the product is not paired: it must be rounded before the sum)
+                        split2(add2(pair2(x[j], x[j + 1]), pair2(-m, -m)), a, b);
+                        split2(add2(pair2(__fmul_rn(a, inv), __fmul_rn(b, inv)), pair2(12582912.0f, 12582912.0f)), a, b);
+                        word += (__float_as_uint(a) << (4 * j)) + (__float_as_uint(b) << (4 * j + 4));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        // clamped first: the bounds are whole numbers, so the rounding commutes with them
+                        const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[j], m), inv), 0.0f), 15.0f);
+                        word += __float_as_uint(__fadd_rn(q, 12582912.0f)) << (4 * j);
+                    }
                 }
                 word -= 0x3F400000u;  // what is left of the eight constants: 0x4B400000 (1 + 16 + 256) modulo 2^32
             }
@@ -181,11 +193,15 @@ __global__ void __launch_bounds__(kKvThreads)
             const int r = row0 + i * (32 / L);
             if (r >= 2 * c.H) continue;
             const float s = kv4_step(pair[i]), m = kv4_low(pair[i]);
+            // code j stays where it is in its half word: 2^23 + c 16^j, so the step is s 16^-j
+            const float sj[4] = {s, s * 0.0625f, s * 0.00390625f, s * 0.000244140625f};
             float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const float code = __uint_as_float(((word[i] >> (4 * j)) & 15u) | 0x4B000000u) - 8388608.0f;  // exact
-                x[j] = __fmaf_rn(s, code, m);
+            for (int j = 0; j < 8; j += 2) {
+                const uint32_t half = j < 4 ? word[i] : word[i] >> 16;
+                const f2 code = add2(pair2u((half & (15u << (4 * (j & 3)))) | 0x4B000000u, (half & (15u << (4 * (j & 3) + 4))) | 0x4B000000u),
+                                     pair2(-8388608.0f, -8388608.0f));  // exact
+                split2(fma2(pair2(sj[j & 3], sj[(j & 3) + 1]), code, pair2(m, m)), x[j], x[j + 1]);
             }
             void *base = r < c.H ? io.k : io.v;
             if (BF) {

@@ -712,6 +712,24 @@ sherry_status few_launch(AttnParams p, cudaStream_t stream) {
 }  // namespace
 }  // namespace sherry
 
+namespace sherry {
+namespace {
+
+// Which kernel is ahead for sequences of more than kFewRows rows, from what the host knows.  The few-row
+// kernel spreads a sequence's pages over the machine but decodes them again for every 16 rows; the tile
+// kernel decodes once for 256 rows, one CTA to a key/value head however long the context.  Measured, per
+// page of context: 0.25 to 0.35 us for 16 rows of a head on one SM, against 1.0 to 1.2 us for 256 (heads
+// of 64 and 128).  E.g. 8 heads, 8,192 tokens, heads of 64: 256 rows 40 us against 133, 1,024 rows 124
+// against 133, 2,048 rows 235 against 134; 32 sequences of 4,096, 32 rows each: 76 against 142.
+bool few_is_faster(const sherry_kv4 *c, int g) {
+    const long long rows = c->T * g, sms = sm_count();
+    const long long few = c->H * (rows / 16 + c->B), tile = c->H * (rows / 256 + c->B);
+    return few * 27 < 100 * sms * ((tile + sms - 1) / sms);
+}
+
+}  // namespace
+}  // namespace sherry
+
 // The parts of the row tiles that the runs of the few-row kernel cut: at most two per run, each
 // with 16 rows of D sums, a maximum and a total.
 extern "C" size_t sherry_attn_kv4_workspace_bytes(int64_t T, int Hq, int D) {
@@ -749,7 +767,7 @@ extern "C" sherry_status sherry_attn_kv4(const sherry_kv4 *c, const uint16_t *q,
     const int64_t most = (c->cu_q ? (max_q > 0 ? std::min(max_q, c->T) : c->T) : 1) * p.g;  // rows of a sequence
     p.wait_limit = wait_limit();
     p.few_rows = 0x7FFFFFFF;
-    if (most > kFewRows) {
+    if (most > kFewRows && !few_is_faster(c, p.g)) {
         // a batch may hold both kinds; a lone sequence is one or the other
         p.few_rows = c->B == 1 ? -1 : kFewRows;
         st = attn_tile_launch(p, c->D, s);

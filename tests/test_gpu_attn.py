@@ -11,13 +11,19 @@ rotation  cos and sin: the fraction of a turn is rounded once (2^-26 turns = 2 p
           quotient and two products add at most 16 u relative: 2^-20, in all (|a| + |b|) 2^-19.
 cache     codes, steps and low ends are equal bit for bit (one rounding after another, in the
           same order); read back, fl32(m + s c) is exact and bf16 rounds that once more.
-attention x_t = scale * q.k_t is summed in fp32 on codes held as 128 + c <= 143: D / 8 sums of
-          16 products, each sum and the two operations after it rounded by at most 2^-23 of the
-          largest partial result, so |dx| <= |scale| * sum|q| * 143 * max s * (D / 8 + 4) * 2^-23
-          plus the low end's share, |m~ - 136 s| <= |m| + 136 s, three roundings.  A probability is off by |dx| and by the exponential's
-          2^-21, so the output by 2 |dx| + 2^-20 times max |v|.  Rounding p s to bf16 moves the
-          output by 2^-8 sum p s |c - 8| <= 2^-8 * 8 * max s_v; the last rounding by 2^-8 |o|;
-          fp32 sums over L tokens by sqrt-free L 2^-23 of max|v| (L <= 2000: 2^-12).
+attention few rows: x_t = scale * q.k_t is summed in fp32 on codes 0 .. 15: D / 8 sums of 16 products,
+          each sum and the operations after it rounded by at most 2^-23 of the largest partial result;
+          |dx| <= |scale| * sum|q| * 2^-23 * (143 * max s * (D / 8 + 4) + 3 (max|m| + 136 max s))
+          covers it (143 and 136 instead of 15: room of a factor of nine).  p s is rounded to fp16: 2^-11 of
+          sum p s c <= 15 max s_v.
+          tiles: keys are rounded to fp16, 2^-11 of each: |dx| <= |scale| * sum|q| * max|k| * 2^-11 more;
+          values and probabilities likewise, 2^-11 of max|v| each (what of them is below fp16's normal
+          range is off by 2^-18 of the page's largest key, 2^-17 of the largest value: below that).
+          A probability is off by |dx| and by the exponential's 2^-21, so the output by 2 |dx| + 2^-20
+          times max |v|; fp32 sums over L tokens by L 2^-23 of max|v| (L <= 2000: 2^-12).  The bound
+          takes 2^-8 * 8 max s_v + 2^-12 max|v| for the roundings of p and v: 2^-5 max s_v is above
+          2^-11 * 15 max s_v, and, where a row of values has both signs (max|v| <= 15 max s_v), above the
+          tiles' 2^-10 max|v| too.  The last rounding is 2^-8 |o|.
 """
 import ctypes
 
@@ -230,18 +236,20 @@ def test_read_makes_its_own_tensors():
 
 
 # ----------------------------------------------------------------------------- attention
-def attn_bound(q, kv, ref, scale):
+def attn_bound(q, kv, ref, scale, tile=False):
     """Per row [n, D]: the bound of the module's head."""
     (k, ks, km), (v, vs, vm) = kv
     D = q.shape[-1]
     sq = np.abs(q).sum(-1, keepdims=True)
     smax, mmax = np.max(ks, initial=0.0), np.max(np.abs(km), initial=0.0)
     dx = abs(scale) * sq * 2.0 ** -23 * (143.0 * smax * (D // 8 + 4) + 3 * (mmax + 136.0 * smax))
+    if tile:
+        dx = dx + abs(scale) * sq * np.max(np.abs(k), initial=0.0) * 2.0 ** -11
     vmax = np.max(np.abs(v), initial=0.0)
     return (2 * dx + 2.0 ** -12) * vmax + 2.0 ** -8 * 8 * np.max(vs, initial=0.0) + 2.0 ** -8 * np.abs(ref)
 
 
-def check_attn(bt, q, out, hq, scale, sentinel=None):
+def check_attn(bt, q, out, hq, scale, sentinel=None, tile=False):
     g = hq // bt.H
     o = np_of(out).astype(np.float64)
     for b, (c, n) in enumerate(zip(bt.ctx, bt.new)):
@@ -251,7 +259,7 @@ def check_attn(bt, q, out, hq, scale, sentinel=None):
             h = j // g
             kv = [(x[h], s[h], m[h]) for x, s, m in bt.kv[b]]
             ref = A.attend(q[r, j].astype(np.float64), kv[0][0], kv[1][0], last, scale)
-            tol = attn_bound(q[r, j], kv, ref, scale)
+            tol = attn_bound(q[r, j], kv, ref, scale, tile)
             err = np.abs(o[r, j] - ref)
             assert np.all(err <= tol), (b, j, np.nanmax(err - tol), np.isnan(err).sum())
             assert not o[r, j][last < 0].any()
@@ -259,7 +267,7 @@ def check_attn(bt, q, out, hq, scale, sentinel=None):
         assert np.all(o[bt.cu[-1]:] == sentinel)
 
 
-def run_attn(ctx, new, hq, H, D, seed, qmag=1.0, scale=None, extra=0, max_q=0, pad=0):
+def run_attn(ctx, new, hq, H, D, seed, qmag=1.0, scale=None, extra=0, max_q=0, pad=0, tile=False):
     bt = Batch(ctx, new, H, D, seed, extra_rows=extra).fill().dev()
     q = bf16_randn(bt.rng, (bt.T, hq, D), qmag)
     big = torch.full((bt.T, hq * D + pad), float("nan"), dtype=BF, device="cuda")
@@ -268,7 +276,7 @@ def run_attn(ctx, new, hq, H, D, seed, qmag=1.0, scale=None, extra=0, max_q=0, p
     out = S.attn_kv4(big[:, :hq * D].unflatten(1, (hq, D)), bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu,
                      max_q=max_q, scale=scale, out=obig[:, :hq * D].unflatten(1, (hq, D)))
     assert S.device_error() == 0
-    check_attn(bt, q, out, hq, D ** -0.5 if scale is None else scale, 77.0 if extra else None)
+    check_attn(bt, q, out, hq, D ** -0.5 if scale is None else scale, 77.0 if extra else None, tile)
     assert pad == 0 or torch.all(obig[:, hq * D:] == 77.0)
     return bt, q, out
 
@@ -294,6 +302,139 @@ def test_attn_longer(ctx, new, hq, H, D):
     for max_q in (0, max(new)):
         run_attn(ctx, new, hq, H, D, seed=len(ctx) * 7 + hq + D, max_q=max_q,
                  extra=0 if all(n == 1 for n in new) else 2)
+
+
+def is_tiles(bt, hq):
+    """The rule by which a batch goes to the tile kernel (sequences of more than 32 rows)."""
+    g, sms = hq // bt.H, torch.cuda.get_device_properties(0).multi_processor_count
+    rows = bt.T * g
+    few, tile = bt.H * (rows // 16 + len(bt.ctx)), bt.H * (rows // 256 + len(bt.ctx))
+    return few * 27 >= 100 * sms * -(-tile // sms)
+
+
+TILES = [
+    ([300], [300], 32, 8), ([700], [300], 32, 8), ([129], [129], 128, 8),
+    ([700, 800, 0, 90], [330, 1, 1, 2], 32, 8),   # a prompt and single tokens: both kernels
+    ([900, 40, 613], [300, 40, 129], 32, 8), ([3, 290], [7, 290], 32, 8),
+    ([1150], [1150], 8, 8), ([400], [400], 24, 8), ([576], [576], 16, 8),
+]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,new,hq,H", TILES)
+def test_attn_tiles(ctx, new, hq, H, D):
+    bt, _, _ = run_attn(ctx, new, hq, H, D, seed=sum(ctx) + D, max_q=max(new) if D == 64 else 0, extra=3, pad=8, tile=True)
+    assert is_tiles(bt, hq)
+
+
+@pytest.mark.parametrize("kw", [dict(qmag=30.0), dict(qmag=1e-4), dict(scale=0.0), dict(scale=-0.3), dict(qmag=1e20, scale=1e-21)])
+def test_attn_tiles_peaked_scores_and_large_values(kw):
+    bt, _, _ = run_attn([433], [330], 32, 8, 64, seed=31, tile=True, **kw)
+    assert is_tiles(bt, 32)
+
+
+@pytest.mark.parametrize("growing", [False, True])
+def test_attn_tiles_values_of_very_different_size(growing):
+    """Values whose size changes a hundredfold from page to page, up or down: O follows their power of two."""
+    bt = Batch([640], [330], 8, 64, seed=32)
+    scale = np.float32(10.0) ** (np.arange(10) if growing else -np.arange(10))
+    bt.fill()
+    vals, s, m = bt.kv[0][1]
+    for h in range(8):
+        for t in range(640):
+            f = scale[t // 64]
+            c, ss, mm = A.kv4_unpack(bt.cache, bt.table[0, t // 64], t % 64, h, 1)
+            s[h, t], m[h, t] = A.to_bf16(np.array([ss, mm]) * f)
+            A.kv4_pack(bt.cache, bt.table[0, t // 64], t % 64, h, 1, c, s[h, t], m[h, t])
+            vals[h, t] = A.kv4_values(c[None], s[h, t:t + 1], m[h, t:t + 1])[0]
+    bt.dev()
+    q = bf16_randn(bt.rng, (bt.T, 32, 64))
+    out = S.attn_kv4(torch.from_numpy(q).cuda().bfloat16(), bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+    assert is_tiles(bt, 32)
+    check_attn(bt, q, out, 32, 0.125, tile=True)
+
+
+def test_attn_tiles_deterministic_and_graph():
+    bt, q, out = run_attn([800, 650], [300, 40], 32, 8, 128, seed=33, tile=True)
+    assert is_tiles(bt, 32)
+    dq = torch.from_numpy(q).cuda().bfloat16()
+    o = torch.empty_like(out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu, out=o)
+    for _ in range(3):
+        o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, out)
+
+
+@pytest.mark.parametrize("bad", [-1, 1 << 20, "width"])
+def test_attn_tiles_bad_pages(bad):
+    new, ctx = 300, [500, 420]
+    bt = Batch(ctx, [new] * 2, 8, 64, seed=34).fill()
+    there = [np.ones(c, bool) for c in ctx]
+    if bad == "width":
+        bt.dev()
+        bt.d_table = bt.d_table[:, :5].contiguous()
+        for t in there:
+            t[320:] = False
+    else:
+        bt.table[0, 1] = bt.table[1, 0] = bad
+        there[0][64:128] = there[1][:64] = False
+        bt.dev()
+    q = bf16_randn(bt.rng, (2 * new, 32, 64))
+    out = S.attn_kv4(torch.from_numpy(q).cuda().bfloat16(), bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+    assert is_tiles(bt, 32) and S.device_error() == 8 and S.device_error() == 0
+    o = np_of(out)
+    for b, c in enumerate(ctx):
+        for j in range(0, 32, 5):
+            kv = [(x[j // 4][there[b]], s[j // 4][there[b]], m[j // 4][there[b]]) for x, s, m in bt.kv[b]]
+            last = np.array([there[b][:c - new + i + 1].sum() - 1 for i in range(new)])
+            r = slice(b * new, (b + 1) * new)
+            ref = A.attend(q[r, j].astype(np.float64), kv[0][0], kv[1][0], last, 0.125)
+            assert np.all(np.abs(o[r, j] - ref) <= attn_bound(q[r, j], kv, ref, 0.125, True))
+
+
+@pytest.mark.parametrize("kv", [0, 1])
+def test_attn_tiles_nan_reaches_only_the_rows_that_see_it(kv):
+    bt = Batch([500], [300], 8, 64, seed=35).fill()
+    at = 64 * 32 + 4 * (400 % 64)
+    bt.cache[bt.table[0, 400 // 64], 3, kv, at:at + 4] = 0xFF    # token 400, head 3
+    bt.dev()
+    q = torch.randn(300, 32, 64, device="cuda").bfloat16()
+    out = S.attn_kv4(q, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+    assert is_tiles(bt, 32)
+    bad = torch.isnan(out).any(-1)      # row i is position 200 + i
+    assert bad[200:, 12:16].all() and not bad[:200].any() and not bad[:, :12].any() and not bad[:, 16:].any()
+
+
+@pytest.mark.parametrize("cu", [[0, -5, 600], [600, 10, 0], [0, 1 << 30, 600], [-9, 300, 1 << 30]])
+def test_attn_tiles_malformed_row_offsets_stay_in_bounds(cu):
+    bt = Batch([700, 690], [300, 300], 8, 64, seed=36).fill().dev()
+    assert is_tiles(bt, 32)
+    q = torch.randn(600, 32, 64, device="cuda").bfloat16()
+    guard = torch.full((602, 32, 64), 77.0, dtype=BF, device="cuda")
+    S.attn_kv4(q, bt.d_cache, bt.d_table, bt.d_lens, cu_q=torch.tensor(cu, dtype=torch.int32, device="cuda"), out=guard[1:601])
+    S.device_error()
+    assert torch.all(guard[0] == 77.0) and torch.all(guard[601] == 77.0)
+
+
+@pytest.mark.parametrize("new", [1, 300])
+def test_waits_that_run_out_are_reported(new):
+    """A limit of a few cycles: the kernels give up, record it and return; the next call is whole again."""
+    bt, q, out = run_attn([700, 690], [new, new], 32, 8, 64, seed=37, tile=new > 1)
+    dq = torch.from_numpy(q).cuda().bfloat16()
+    S.set_wait_limit(16)
+    try:
+        for _ in range(2):
+            S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+        # a copy of a page or two may well be there at the first look; the tiles' first product is not
+        assert S.device_error() in ((6,) if new > 1 else (0, 6))
+    finally:
+        S.set_wait_limit(0)
+    assert S.device_error() == 0
+    assert torch.equal(S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu), out)
 
 
 @pytest.mark.parametrize("new", [[1], [140]])

@@ -21,8 +21,7 @@ namespace {
 // per key/value head fill half of the instruction instead of a quarter.
 // Decoding is what bounds it next (integer instructions, half of an SM's rate): a code's four bits at the
 // bottom of a half word are the fp16 c 2^-24, one up c 2^-20, so a word of eight codes takes a shift and
-// four ANDs; the powers of two go into q (fp16, exact after a power of two per row) and into the last
-// factor of the result.
+// four ANDs; the keys' powers of two go into q (fp16, exact after a power of two per row).
 // Earlier forms, 32 sequences of 32,768 tokens with heads of 128 (floor 177 us): a page shared by four
 // warps and filled by a fifth, 357 us; a warp per page with codes as bf16 128 + c (a shift and an OR
 // more per pair), 320 us.
@@ -330,6 +329,10 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             if (!dead && there[s] && t0 <= last_max) {
                 const uint8_t *kb = ring + s * F::kStage, *vb = kb + Kv4<D>::kBlock;
                 const bool whole = t0 + SHERRY_KV4_PAGE - 1 <= last_min;
+                const uint32_t a1[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+                float ones[NT][4];                            // sums of the page's p s
+#pragma unroll
+                for (int t = 0; t < NT; t++) ones[t][0] = ones[t][1] = ones[t][2] = ones[t][3] = 0.0f;
 #pragma unroll 1
                 for (int q0 = 0; q0 < 4; q0 += kTiles) {
                 float x[kTiles][NT][4];                       // scores of tiles of 16 tokens
@@ -371,18 +374,18 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                             for (int j = 0; j < 2; j++)
                                 x[qi][t][2 * i + j] = kv4_step(kp[i]) * x[qi][t][2 * i + j] + kv4_low(kp[i]) * qsum[t][j];
                 }
-                float sv[kTiles][2], mv[kTiles][2];           // steps and low ends of the values
+                float sv[kTiles][2], mv[kTiles][2];           // steps and centres of the values
 #pragma unroll
                 for (int qi = 0; qi < kTiles; qi++)
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
                         const uint32_t vp = reinterpret_cast<const uint32_t *>(vb + Kv4<D>::kCodes)[16 * (q0 + qi) + tok_r + 8 * i];
                         sv[qi][i] = kv4_step(vp);
-                        mv[qi][i] = kv4_low(vp);
+                        mv[qi][i] = kv4_low(vp) + 8.0f * sv[qi][i];
                     }
                 if (!whole) {
                     // A token that a row does not see may hold anything: its probability is 2^-inf, and a step or
-                    // low end that is not a number goes to the score of the rows that do see it.
+                    // centre that is not a number goes to the score of the rows that do see it.
 #pragma unroll
                     for (int qi = 0; qi < kTiles; qi++)
 #pragma unroll
@@ -456,6 +459,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                             ref[t][j] = (mx == -INFINITY ? 0.0f : mx * sc[t][j]) - (kUp - (float)ve);
                             l[t][j] *= f;
                             corr[t][j] *= f;
+                            ones[t][j] *= f;
 #pragma unroll
                             for (int i = 0; i < MT; i++) {
                                 o[t][i][j] *= f;
@@ -496,8 +500,24 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                             for (int t = 0; t < NT; t++) mma_f16(o[t][4 * w + i], a, pb[qi][t][0], pb[qi][t][1]);
                         }
                     }
+#pragma unroll
+                    for (int t = 0; t < NT; t++) mma_f16(ones[t], a1, pb[qi][t][0], pb[qi][t][1]);
                 }
                 }
+                // The tensor cores' sums round towards zero, and a long sum of codes 0 .. 15 drifts (32,768 tokens
+                // came out at twice the error of a bf16 result): the page's 8 sum(p s) comes off again, so that the
+                // sums stay small.  (Codes less 8 as operands cost an instruction per pair: 251 us against 212.)
+#pragma unroll
+                for (int t = 0; t < NT; t++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        const float e0 = ones[t][j] * -4.76837158203125e-07f, e1 = ones[t][j] * -7.62939453125e-06f;  // -8 2^-24, -8 2^-20
+#pragma unroll
+                        for (int i = 0; i < MT; i++) {
+                            o[t][i][j] += i & 1 ? e1 : e0;
+                            o[t][i][2 + j] += i & 1 ? e1 : e0;
+                        }
+                    }
             }
             __syncwarp();
             if (lane == 0 && !dead) copy_next();

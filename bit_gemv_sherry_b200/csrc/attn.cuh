@@ -4,7 +4,7 @@
 //     out = sum_t p_t v_t / sum_t p_t,   p_t = 2^(x_t - m),   x_t = scale log2(e) (q . k_t).
 // With k_t = m_t + s_t c_t and c_t in 0 .. 15,  q . k_t = s_t (q . c_t) + m_t sum(q): the first
 // product runs on the codes, which fp16 holds exactly, and the step and low end come in after it.
-// Likewise sum_t p_t v_t = sum_t (p_t s_t) c_t + sum_t p_t m_t.
+// Likewise sum_t p_t v_t = sum_t (p_t s_t) (c_t - 8) + sum_t p_t (m_t + 8 s_t).
 #pragma once
 
 #include <cuda_bf16.h>

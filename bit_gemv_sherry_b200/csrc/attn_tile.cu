@@ -15,18 +15,26 @@
 // makes the value.  Queries are bf16: a power of two per row makes them exact in fp16.
 // Probabilities are fp16 of values up to 2^15, the row's maximum at 2^10 or above: relative 2^-11
 // down to 2^-24 of the largest.
-// Earlier forms, per step with heads of 128: codes as operands and steps and low ends applied to S
-// and P by the softmax threads, whose scales came from shared memory (8,000 clocks: 128 16-byte
-// loads a row in the way of the products' operand reads); unrolled over the whole step (7,000:
-// four roles' straight-line code does not fit the instruction cache, every role ran at six clocks
-// an instruction).
 // Roles: warps 0-3 and 4-7 the softmax of a tile each (a thread owns a row: no shuffles), warps
 // 8-9 decode keys, 10-11 values, warp 12 issues the products, 13 copies pages (codes of keys and
 // values of a page are one bulk copy).  The tiles alternate: while one's softmax runs, the tensor
 // cores work for the other.
-// The bounds: the exponentials (16 a clock and SM: 2048 clocks per 256 x 128 scores), the products
-// (1024 clocks for heads of 64, 2048 for 128) and shared memory (decoded operands written once and
-// read by the products: 1152 and 2048 clocks at 128 bytes a clock).
+// The bounds, in clocks per 256 rows and 128 tokens (heads of 64; 128): the exponentials 2,048 (16 a clock
+// and SM), the products 1,024; 2,048, shared memory 1,150; 2,300 (decoded operands written once and read
+// by the products, whose scores alone take all of its bandwidth while they run).  Measured: 3,900; 4,500.
+// A tile's softmax (about 2,300 clocks with two of them on the exponentials' unit) and its products (600;
+// 1,300) follow each other, and the other tile fills only part of the gap.  4 prompts' chunks of 4,096 tokens
+// at 16,384, 32 heads of 128 over 8: 3.9 ms, 960 TFLOP/s; a prompt of 2,048, heads of 64: 47 us.
+// Tried, in clocks per step with heads of 128 unless said otherwise:
+//   codes as operands, steps and low ends applied by the softmax threads from shared memory: 8,000
+//   the present operands, code unrolled over the step (four roles' straight-line code does not fit the
+//     instruction cache, every role ran at six clocks an instruction): 7,000; a pass of its own for the
+//     maximum: 5,000
+//   one branch-free step of 128 columns with a test at its end: the same, slower for short prompts
+//   two S of 64 columns for each tile, so that neither side waits: 5,000 (products of 64 columns and twice
+//     the hand-overs cost more than the waiting)
+//   P beside S (there is room for heads of 64), the next scores issued early: 3,900 to 4,200 for heads of 64
+//   a share of the exponentials as polynomials on the FMA pipe: 1 in 8 1% slower, 3 in 8 5% slower
 #include <algorithm>
 
 #include "attn.cuh"
@@ -691,7 +699,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             auto scores = [&](int i, int s) {  // S_i = Q_i K^T
                 tc_fence_after();
                 if (elect_one()) {
-mma_ss_all<0, D / 16, 128>(tmem + i * kKeys, q_lo + i * (T::kQ >> 4), k_lo + s * (T::kOp >> 4), kIdesc<kKeys>);
+                    mma_ss_all<0, D / 16, 128>(tmem + i * kKeys, q_lo + i * (T::kQ >> 4), k_lo + s * (T::kOp >> 4), kIdesc<kKeys>);
                     umma_commit(&bar->s_full[i]);
                 }
                 __syncwarp();

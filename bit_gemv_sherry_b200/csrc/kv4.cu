@@ -101,7 +101,8 @@ __device__ __forceinline__ void row_range(const uint4 (&u)[BF ? 1 : 2], const fl
 // looked up once, and all of the warp's loads are under way before the first is used.  One read and one
 // write per element bound it, if the conversions keep to the fast pipes: a code becomes a float, and a
 // float a code, by adding 2^23 or 1.5 2^23 (the conversion instructions run at a quarter of the rate:
-// 32,768 tokens with heads of 128 took 84 us to write and 63 to read with them).
+// 32,768 tokens of 8 heads of 128 took 139 us to write and read with them, 82 without; instruction issue,
+// 70 to 80% busy, is what bounds it now, above the 53 us of its bytes).
 template <int D, int STEPS>
 __host__ __device__ constexpr int rows_per_warp() { return STEPS * 32 / (D / 8); }
 
@@ -238,7 +239,8 @@ void rows_launch_steps(const Kv4View &c, const KvIo &io, unsigned int *err, cuda
 
 template <int D, bool BF, bool WRITE>
 void rows_launch(const Kv4View &c, const KvIo &io, unsigned int *err, cudaStream_t stream) {
-    // Few rows: one step per warp, for the latency; many: four, for the loads under way.
+    // Few rows: one step per warp, for the latency (16 tokens of 8 heads of 64, written and read: 3.5 us
+    // against 5.7); many: four, for the loads under way (32,768 tokens: 82 us).
     if ((long long)c.T * 2 * c.H * (D / 8) / 32 < kManySteps) rows_launch_steps<D, BF, WRITE, 1>(c, io, err, stream);
     else rows_launch_steps<D, BF, WRITE, 4>(c, io, err, stream);
 }

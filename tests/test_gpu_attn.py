@@ -571,6 +571,31 @@ def test_nan_in_a_visible_token_reaches_only_its_rows():
     assert bad[0, 2:].all() and not bad[0, :2].any() and not bad[1].any()
 
 
+@pytest.mark.parametrize("kv", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_among_drafts_reaches_only_the_rows_that_see_it(kv, D):
+    bt = Batch([70, 9], [5, 2], 2, D, seed=17).fill()
+    at = 32 * D + 4 * 3
+    bt.cache[bt.table[0, 1], 1, kv, at:at + 4] = 0xFF    # token 67 of sequence 0, head 1: seen by rows 2, 3, 4
+    bt.dev()
+    q = torch.randn(7, 6, D, device="cuda").bfloat16()
+    out = S.attn_kv4(q, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu, max_q=5)
+    bad = torch.isnan(out).any(-1)
+    assert bad[2:5, 3:].all() and not bad[:2].any() and not bad[5:].any() and not bad[:, :3].any()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_context_keeps_bf16_accuracy(D):
+    """A bf16 rounding is off by at most 2^-8 / sqrt(12) * 2 of a value (rms of half a step either way, where
+    the value's mantissa is smallest); everything before it together by less than 2^-12."""
+    bt, q, out = run_attn([20000], [1], 8, 2, D, seed=23)
+    for j in range(0, 8, 3):
+        kv = [(x[j // 4], s[j // 4], m[j // 4]) for x, s, m in bt.kv[0]]
+        ref = A.attend(q[:, j].astype(np.float64), kv[0][0], kv[1][0], [19999], D ** -0.5)
+        err = np.linalg.norm(np_of(out)[0, j] - ref[0]) / np.linalg.norm(ref[0])
+        assert err <= 2.0 ** -7 / 12 ** 0.5 + 2.0 ** -12
+
+
 # ----------------------------------------------------------------------------- together
 @pytest.mark.parametrize("D,hq,H", [(64, 8, 2), (128, 4, 2)])
 def test_attention_block_between_gemvs(D, hq, H):

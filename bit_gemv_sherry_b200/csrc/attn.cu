@@ -1,6 +1,7 @@
 // attn.cu -- causal attention over the 4-bit key/value cache: the calls, and the kernels for
 // sequences with few new tokens (decode steps, drafts).
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.cuh"
 
@@ -13,9 +14,10 @@ namespace {
 // The bytes of the cache are the bound: 2 (D / 2 + 4) per token and head.  The work is the pages of the
 // batch in the order (sequence, head, row tile, page), a row tile being up to 8 NT rows (query heads that
 // share a key/value head, times new tokens).  It is cut into equal runs, one per warp, so that long and
-// short sequences load the machine alike (and as few runs as that takes: fewer parts to join); row tiles that a run does not hold whole go to the workspace
-// and a second kernel joins their parts in the order of the runs (no atomics: results do not depend on
-// timing).  A warp works alone: it copies its pages into its own ring (a page's keys and values are one
+// short sequences load the machine alike (and as few runs as that takes: fewer parts to join); row tiles
+// that a run does not hold whole go to the workspace and a second kernel joins their parts in the order of
+// the runs (no atomics: results do not depend on timing).  Few row tiles of few pages go to a cluster each
+// instead, which joins its warps' parts in shared memory.  A warp works alone: it copies its pages into its own ring (a page's keys and values are one
 // contiguous block: one bulk copy), and no other warp waits for it.
 // The product is S^T = K q^T, 16 tokens by 8 rows: the 8-wide side carries the few rows, so 4 query heads
 // per key/value head fill half of the instruction instead of a quarter.
@@ -26,7 +28,7 @@ namespace {
 // instructions a page, two thirds of them integer.  Earlier forms: a page shared by four warps and filled
 // by a fifth, 357 us; a warp per page with codes as bf16 128 + c (a shift and an OR more per pair), 320 us;
 // selects for unseen tokens on every page and 64-bit divisions in the walk, 234 us.  Short contexts are
-// latency: one page 5.9 us, a second kernel to join parts 3 us more.
+// latency: two pages 5.8 us as a cluster, 8.8 as runs and a join.
 constexpr int kFewWarps = 4;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewRunsMax = 2560;  // bounds the workspace
@@ -34,6 +36,7 @@ constexpr int kFewRows = 32;       // rows of a sequence up to which this kernel
 // Starting and ending a row tile costs a warp about as much as this many pages; counted as work where
 // there is enough of it.
 constexpr int kUnitCost = 1;
+constexpr int kJoinPages = 3;
 
 template <int D, int NT>
 struct Few {
@@ -184,9 +187,28 @@ constexpr float kUp = 7.0f;
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
 
-template <int D, int NT>
+// CL > 0: a cluster of CL CTAs takes one row tile, its warps every 4 CL-th page each, and their parts meet
+// through distributed shared memory: no second kernel.  For few row tiles of few pages (see few_launch).
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address of this CTA's shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_address(uint32_t addr, int rank) {
+    uint32_t d;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(addr), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ float peer_load(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int D, int NT, int CL>
 __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_kernel(const __grid_constant__ AttnParams p) {
     using F = Few<D, NT>;
+    constexpr int kCl = CL ? CL : 1;
+    constexpr int kStep = CL ? CL * kFewWarps : 1;  // pages from one of a warp to its next
     constexpr int kRows = F::kRows, kS = F::kStages, MT = D / 16, WK = D / 32, kTiles = F::kTiles;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -206,21 +228,36 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");  // lengths and cache come from the kernels before
-    const Work work = all_work<kRows>(p);
-    const int run = blockIdx.x + gridDim.x * warp;      // neighbouring runs on different SMs
-    const long long from = run * work.each, to = min(from + work.each, work.total);
-    if (from >= to) return;
+    int run = 0;
     Walk<kRows> walk;
-    walk.start(p, work, from, to);
+    if (CL) {
+        long long units;
+        find_seq<kRows, true>(p, Work{}, blockIdx.x / kCl, walk.b, units);
+        if (walk.b >= p.c.B) return;  // the whole cluster
+        walk.s = seq_work<kRows>(p, walk.b);
+        const int unit = (int)(blockIdx.x / kCl - units);
+        walk.h = unit / walk.s.tiles;
+        walk.tile = unit - walk.h * walk.s.tiles;
+        walk.page0 = (int)(blockIdx.x % kCl) * kFewWarps + warp;
+        walk.page1 = walk.s.pages;
+        if (threadIdx.x == 0 && walk.s.len > p.c.width * SHERRY_KV4_PAGE) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
+    } else {
+        const Work work = all_work<kRows>(p);
+        run = blockIdx.x + gridDim.x * warp;  // neighbouring runs on different SMs
+        const long long from = run * work.each, to = min(from + work.each, work.total);
+        if (from >= to) return;
+        walk.start(p, work, from, to);
+    }
 
     int copied = 0, to_copy = 0;
     if (lane == 0) {
         ahead = walk;
-        ahead.page1 = ahead_page = 0;
+        ahead_page = walk.page0;
+        if (!CL) ahead.page1 = ahead_page = 0;
     }
     auto copy_next = [&]() {
         while (ahead_page >= ahead.page1) {
-            if (!ahead.next(p)) return;
+            if (CL || !ahead.next(p)) return;
             ahead_page = ahead.page0;
             if (ahead.s.len > p.c.width * SHERRY_KV4_PAGE) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
         }
@@ -233,7 +270,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
         } else {
             mbar_arrive(full + s);
         }
-        ahead_page++;
+        ahead_page += kStep;
         copied++;
         to_copy = to_copy + 1 == kS ? 0 : to_copy + 1;
     };
@@ -250,7 +287,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
     int it = 0, s = 0;        // pages done, ring slot of the next
     uint32_t lap = 0;         // its phase
     bool dead = false;
-    while (walk.next(p)) {
+    for (bool more = CL || walk.next(p); more; more = !CL && walk.next(p)) {
         const int nrow = walk.s.rows * p.g, row0 = walk.tile * kRows;
         const int pos0 = walk.s.len - walk.s.rows;            // position of the first new token
         // q: lane (r, c) holds elements [c D / 4, (c + 1) D / 4) of row r of each row group
@@ -325,7 +362,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
 #pragma unroll
             for (int j = 0; j < 2; j++) m[t][j] = -INFINITY, ref[t][j] = 0.0f, l[t][j] = 0.0f, corr[t][j] = 0.0f;
         }
-        for (int pg = walk.page0; pg < walk.page1; pg++, it++) {
+        for (int pg = walk.page0; pg < walk.page1; pg += kStep, it++) {
             dead = dead || !__all_sync(0xFFFFFFFFu, mbar_wait(full + s, lap, abort, p.err, p.wait_limit));
             const int t0 = pg * SHERRY_KV4_PAGE;              // first token of the page
             if (!dead && there[s] && t0 <= last_max) {
@@ -543,6 +580,60 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                     o[t][i][2 + j] = o[t][i][2 + j] * f + corr[t][j];
                 }
             }
+        if (CL) {
+            if (dead && lane == 0) {
+                // copies in flight land before their memory is used again
+                volatile int no_abort = 0;
+                for (int j = max(it, copied - kS); j < copied; j++)
+                    mbar_wait(full + j % kS, (j / kS) & 1, &no_abort, p.err, 1000000000LL);
+            }
+            __syncwarp();
+            // each warp's part into its own ring: [row][D] sums, then the rows' references and totals
+            float *part = reinterpret_cast<float *>(ring);
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const int row = 8 * t + 2 * c + j;
+#pragma unroll
+                    for (int i = 0; i < MT; i += 4)
+#pragma unroll
+                        for (int k = 0; k < 2; k++)
+                            *reinterpret_cast<float4 *>(part + row * D + r * (D / 8) + 2 * i + 4 * k) =
+                                make_float4(o[t][i][2 * k + j], o[t][i + 1][2 * k + j], o[t][i + 2][2 * k + j],
+                                            o[t][i + 3][2 * k + j]);
+                    if (r == 0)
+                        reinterpret_cast<float2 *>(part + kRows * D)[row] =
+                            make_float2(m[t][j] == -INFINITY ? -INFINITY : ref[t][j], l[t][j]);
+                }
+            cluster_sync();
+            // the cluster's CTAs share the rows; lane i holds the weight of part i, the parts in order
+            constexpr int kParts = kCl * kFewWarps, kMine = kRows / kCl;
+            static_assert(kParts <= 32 && kMine * kCl == kRows, "a lane per part");
+            const uint32_t mine = smem_u32(smem);
+            const int part_i = lane % kParts;
+            const uint32_t from = peer_address(mine + (part_i % kFewWarps) * kS * F::kStage, part_i / kFewWarps);
+            for (int n = warp; n < kMine * (D / 32); n += kFewWarps) {
+                const int row = (int)(blockIdx.x % kCl) * kMine + n / (D / 32), d = n % (D / 32) * 32 + lane, rw = row0 + row;
+                const float pm = peer_load(from + (kRows * D + 2 * row) * 4), pl = peer_load(from + (kRows * D + 2 * row + 1) * 4);
+                float mx = pm;
+#pragma unroll
+                for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
+                // a part without keys has sum 0; a NaN among its scores shows in the sum
+                const float f = pm == -INFINITY ? (pl == 0.0f ? 0.0f : pl) : exp2_fast(pm - mx);
+                float sum = lane < kParts ? pl * f : 0.0f, acc = 0.0f;
+#pragma unroll
+                for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+#pragma unroll 16
+                for (int k = 0; k < kParts; k++)
+                    acc += __shfl_sync(0xFFFFFFFFu, f, k) * peer_load(__shfl_sync(0xFFFFFFFFu, from, k) + (row * D + d) * 4);
+                if (rw < nrow)
+                    p.out[(long long)(walk.s.first + rw / p.g) * p.out_stride + (long long)(walk.h * p.g + rw % p.g) * D + d] =
+                        __bfloat16_as_ushort(__float2bfloat16_rn(sum == 0.0f ? 0.0f : acc * (1.0f / sum)));
+            }
+            cluster_sync();  // no CTA leaves while its memory is read
+            return;
+        }
         const bool all = walk.page0 == 0 && walk.page1 == walk.s.pages;
         // parts of a row tile: slot 1 of the run that holds its first page, slot 0 of the others
         const long long slot = 2LL * run + (walk.page0 == 0 ? 1 : 0);
@@ -691,17 +782,21 @@ int few_blocks_per_sm(K kernel, size_t smem, OccupancyCache &cache) {
 }
 
 template <typename K>
-void launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const AttnParams &p) {
+void launch_after(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const AttnParams &p, int cluster = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -709,20 +804,41 @@ template <int D, int NT>
 sherry_status few_launch(AttnParams p, cudaStream_t stream) {
     using F = Few<D, NT>;
     static OccupancyCache cache;
-    const int bps = few_blocks_per_sm(attn_few_kernel<D, NT>, F::kSmem, cache);
-    const int ctas = std::min(sm_count() * bps, kFewRunsMax / kFewWarps);
-    p.grid = ctas * kFewWarps;  // runs
-    launch_after(attn_few_kernel<D, NT>, dim3((unsigned)ctas), kFewThreads, F::kSmem, stream, p);
-    const sherry_status st = launch_status("sherry_attn_kv4");
-    // a table of one page cuts nothing
-    if (st != SHERRY_OK || p.c.width == 1) return st;
+    const int bps = few_blocks_per_sm(attn_few_kernel<D, NT, 0>, F::kSmem, cache);
     // at most this many row tiles
     long long tiles = (long long)p.c.T * p.g / F::kRows + p.c.B;
     if (p.few_rows < 0x7FFFFFFF)
         tiles = std::min(tiles, (long long)p.c.B * ((p.few_rows + F::kRows - 1) / F::kRows));
     if (!p.c.cu) tiles = (long long)p.c.B * ((p.g + F::kRows - 1) / F::kRows);
+    // and with the rows shared out evenly this many
+    const long long even = std::min(tiles, ((long long)p.c.T * p.g / p.c.B + F::kRows - 1) / F::kRows * p.c.B) * p.c.H;
     tiles *= p.c.H;
-    if (tiles > 0x7FFFFFFF) return SHERRY_ERR_UNSUPPORTED;
+    if (tiles > 0x7FFFFFFF / 8) return SHERRY_ERR_UNSUPPORTED;
+    // A cluster per row tile, or equal runs and a join.  In pages one after the other, if every sequence is as
+    // long as its table: the largest cluster of which all are resident at once, against the runs and about
+    // kJoinPages for the join and its launch.  Clusters and runs, us, one new token and 8 heads each: one
+    // sequence of 2,048 tokens, heads of 64, 6.4 and 10.9; of 8,192, 10.3 and 14.5; 16 of 2,048, heads of 128,
+    // 19.2 and 22.6 (clusters of 2; of 8, in more than one wave, 30.7); 64 of 1,024, heads of 64, in waves
+    // 59.5 and 26.0.
+    const long long slots = (long long)sm_count() * bps, width = p.c.width;
+    const long long by_runs = (even * width + slots * kFewWarps - 1) / (slots * kFewWarps) + kJoinPages;
+    auto clusters = [&](auto size) {
+        constexpr int CL = decltype(size)::value;
+        if (width == 1 || even * CL > slots || (width + CL * kFewWarps - 1) / (CL * kFewWarps) > by_runs) return false;
+        static OccupancyCache cluster_cache;
+        few_blocks_per_sm(attn_few_kernel<D, NT, CL>, F::kSmem, cluster_cache);
+        launch_after(attn_few_kernel<D, NT, CL>, dim3((unsigned)(tiles * CL)), kFewThreads, F::kSmem, stream, p, CL);
+        return true;
+    };
+    if (clusters(std::integral_constant<int, 8>{}) || clusters(std::integral_constant<int, 4>{}) ||
+        clusters(std::integral_constant<int, 2>{}))
+        return launch_status("sherry_attn_kv4");
+    const int ctas = std::min(sm_count() * bps, kFewRunsMax / kFewWarps);
+    p.grid = ctas * kFewWarps;  // runs
+    launch_after(attn_few_kernel<D, NT, 0>, dim3((unsigned)ctas), kFewThreads, F::kSmem, stream, p);
+    const sherry_status st = launch_status("sherry_attn_kv4");
+    // a table of one page cuts nothing
+    if (st != SHERRY_OK || p.c.width == 1) return st;
     // Up to about this many parts a row tile: four warps a row for one long sequence (24 us against 36 at
     // 32,768 tokens, heads of 64), one for many (29 us against 41 for 64 sequences of 1,024).
     const long long parts = std::min<long long>(p.grid / tiles, p.c.width);

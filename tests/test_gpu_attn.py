@@ -127,11 +127,11 @@ def test_rope_zero_rows_and_nan_stay_in_their_row():
 class Batch:
     """Sequences in shuffled pages; unused slots, pages and table entries hold poison."""
 
-    def __init__(self, ctx, new, H, D, seed, extra_rows=0, spare=2):
+    def __init__(self, ctx, new, H, D, seed, extra_rows=0, spare=2, wide=0):
         rng = self.rng = np.random.default_rng(seed)
         self.ctx, self.new, self.H, self.D = ctx, new, H, D
         need = [(c + 63) // 64 for c in ctx]
-        self.width = max(max(need), 1) + 1
+        self.width = max(max(need) + 1, 2, wide)
         self.pages = sum(need) + spare
         order = rng.permutation(self.pages)
         self.table = np.full((len(ctx), self.width), -7, np.int32)
@@ -267,8 +267,8 @@ def check_attn(bt, q, out, hq, scale, sentinel=None, tile=False):
         assert np.all(o[bt.cu[-1]:] == sentinel)
 
 
-def run_attn(ctx, new, hq, H, D, seed, qmag=1.0, scale=None, extra=0, max_q=0, pad=0, tile=False):
-    bt = Batch(ctx, new, H, D, seed, extra_rows=extra).fill().dev()
+def run_attn(ctx, new, hq, H, D, seed, qmag=1.0, scale=None, extra=0, max_q=0, pad=0, tile=False, wide=0):
+    bt = Batch(ctx, new, H, D, seed, extra_rows=extra, wide=wide).fill().dev()
     q = bf16_randn(bt.rng, (bt.T, hq, D), qmag)
     big = torch.full((bt.T, hq * D + pad), float("nan"), dtype=BF, device="cuda")
     big[:, :hq * D] = torch.from_numpy(q).reshape(bt.T, hq * D)
@@ -302,6 +302,79 @@ def test_attn_longer(ctx, new, hq, H, D):
     for max_q in (0, max(new)):
         run_attn(ctx, new, hq, H, D, seed=len(ctx) * 7 + hq + D, max_q=max_q,
                  extra=0 if all(n == 1 for n in new) else 2)
+
+
+# Short tables go to a cluster per row tile where the batch has few; a table of this width (what a sequence
+# may grow to) and a batch of many row tiles go to runs over the whole machine and a join.
+WIDE = 4096
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,new,hq,H", [
+    ([1], [1], 4, 1), ([1500], [1], 4, 1), ([900, 17, 1300, 0, 64], [1] * 5, 8, 2), ([200, 1, 0, 63, 128], [1] * 5, 8, 8),
+    ([70, 5, 0, 64, 300], [9, 5, 2, 1, 17], 20, 1), ([130], [130], 6, 2), ([3, 2], [7, 2], 16, 1),
+])
+def test_attn_in_runs(ctx, new, hq, H, D):
+    one = all(n == 1 for n in new)
+    args = dict(hq=hq, H=H, D=D, seed=sum(ctx) + hq, extra=0 if one else 3, max_q=0 if D == 64 else max(new), pad=8)
+    _, _, out = run_attn(ctx, new, wide=WIDE, **args)
+    _, _, short = run_attn(ctx, new, **args)     # the same numbers, the sums in another order
+    rows = sum(new)
+    assert torch.allclose(out[:rows].float(), short[:rows].float(), rtol=2.0 ** -7, atol=2.0 ** -10 * short[:rows].abs().max().item())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,new,hq,H", [(5, 1, 32, 8), (11, 1, 32, 8), (24, 1, 8, 8), (50, 1, 8, 8), (90, 1, 16, 8), (13, 5, 32, 8), (26, 3, 32, 8),
+                                        (45, 3, 32, 8)])
+def test_attn_batches_of_every_cluster_size(n, new, hq, H, D):
+    ctx = [[70, 1, 129, 0, 64, 200, 3][i % 7] for i in range(n)]
+    run_attn(ctx, [new] * n, hq, H, D, seed=n + D, max_q=new)
+
+
+def test_attn_in_runs_is_deterministic_and_graph_safe():
+    bt, q, out = run_attn([800, 650, 150], [1] * 3, 8, 2, 64, seed=11, wide=WIDE)
+    dq = torch.from_numpy(q).cuda().bfloat16()
+    outs, graphs = [torch.empty_like(out) for _ in range(2)], []
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(5):
+                S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, out=o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, out) for o in outs)
+    bt.d_lens.copy_(torch.tensor([800, 64, 1], dtype=torch.int32))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens))
+    assert S.device_error() == 0
+
+
+@pytest.mark.parametrize("kv", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attn_in_runs_nan_and_bad_pages(kv, D):
+    bt = Batch([70, 900], [5, 2], 2, D, seed=17, wide=WIDE).fill()
+    at = 32 * D + 4 * 3
+    bt.cache[bt.table[0, 1], 1, kv, at:at + 4] = 0xFF    # token 67 of sequence 0, head 1: seen by rows 2, 3, 4
+    bt.dev()
+    q = torch.randn(7, 6, D, device="cuda").bfloat16()
+    out = S.attn_kv4(q, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu, max_q=5)
+    bad = torch.isnan(out).any(-1)
+    assert bad[2:5, 3:].all() and not bad[:2].any() and not bad[5:].any() and not bad[:, :3].any()
+    assert S.device_error() == 0
+    bt.d_table[0, 1] = bt.pages      # that page away: tokens 0 .. 63 are left
+    out = S.attn_kv4(q, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu, max_q=5)
+    assert S.device_error() == 8 and not torch.isnan(out).any()
+    q = q.float().cpu().numpy().astype(np.float64)
+    for j in range(6):
+        part = [(x[j // 3][:64], s[j // 3][:64], m[j // 3][:64]) for x, s, m in bt.kv[0]]
+        ref = A.attend(q[:5, j], part[0][0], part[1][0], [63] * 5, D ** -0.5)
+        assert np.all(np.abs(np_of(out)[:5, j] - ref) <= attn_bound(q[:5, j], part, ref, D ** -0.5))
 
 
 def is_tiles(bt, hq):

@@ -5,12 +5,13 @@
 // (a cos - b sin, b cos + a sin).  One read and one write per element: the bound
 // is HBM, and for a few tokens the launch.
 //
-// One CTA per token: the R / 2 angles are made once (64-bit product and reduction to a fraction of a
-// turn, then fp32 sincospi) and shared by all heads, while the first rows are on their way.  Eight
-// consecutive elements per lane where R / 2 is a multiple of 8, else four: a lane's partner elements then
-// lie in one other lane of the row.  8,191 tokens of 40 heads of 128 in bf16, normed: 36 us, 4.7 TB/s
-// (four elements a lane, nothing loaded ahead: 59 us; a warp per token, angles in registers: 38 us, and
-// with four rows under way 37 us and 13 instead of 7 for 2,048 tokens in fp32).  One token: 1.7 us.
+// A CTA takes one token or four: their R / 2 angles each are made once (64-bit product and reduction to a
+// fraction of a turn, then fp32 sincospi) and shared by all heads, while the first rows are on their way.
+// A lane holds both elements of its pairs, 16 bytes of bf16 from either half (8 where R / 2 is no multiple
+// of 8).  8,191 tokens of 40 heads of 128 in bf16, normed, half of each head turned: 31 us, 5.4 TB/s, which
+// is HBM's within a fifth; 2,048 tokens of 40 heads of 64, fp32: 5.1 us; one token: 1.7 us.  Earlier forms of
+// the first: partner elements by shuffles, one token a CTA, 36 us; a warp per token 38 us; three CTAs per SM
+// 34 us (fewer loads under way), five 43 us (spills).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -19,6 +20,8 @@ namespace sherry {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeCtas = 4;    // per SM
+constexpr int kRopeTokens = 4;  // of a CTA
 constexpr int kRopeMaxD = 256;
 
 struct RopeSide {
@@ -33,8 +36,9 @@ struct RopeParams {
     RopeSide side[2];  // queries, keys
     const int *positions;
     const float *inv_freq;
-    int D, R;
+    int T, D, R;
     int interleaved;
+    int step_rows;  // rows of a token, up to a warp's whole steps
     float eps;
 };
 
@@ -98,148 +102,182 @@ __device__ __forceinline__ void store_floats(void *base, long long at, const flo
     }
 }
 
-// LP lanes per row (a power of two), NC chunks of E LP elements per row.
-template <bool IN_BF, bool OUT_BF, int E, int LP, int NC>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    __shared__ __align__(16) float2 cs[kRopeMaxD / 2];  // (cos, sin) of the token's angles
+// LP lanes per row (a power of two), two chunks of E elements each: E pairs, so that a lane turns them by itself.
+template <bool IN_BF, bool OUT_BF, int E, int LP, int TOKENS>
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ __align__(16) float cos_of[TOKENS][kRopeMaxD / 2], sin_of[TOKENS][kRopeMaxD / 2];  // of the tokens' angles
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kRows = 32 / LP;        // rows of a warp
-    const long long t = blockIdx.x;
+    const int t0 = blockIdx.x * TOKENS, tokens = min(TOKENS, p.T - t0);
     const int half = p.R / 2;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sub = lane & (LP - 1), base = lane - sub;
-    const int heads = p.side[0].heads + p.side[1].heads;
-    const bool any_weight = p.side[0].weight || p.side[1].weight;
-    const float inv_d = 1.0f / (float)p.D;
-    // where a lane's first element of a row is, per side (head h at + h D)
-    const long long in0 = t * p.side[0].in_stride + E * sub, in1 = t * p.side[1].in_stride - p.side[0].heads * p.D + E * sub;
-    const long long out0 = t * p.side[0].out_stride + E * sub, out1 = t * p.side[1].out_stride - p.side[0].heads * p.D + E * sub;
-    auto load = [&](int r0, Raw<IN_BF, E> (&v)[NC]) {
-        const int r = r0 + lane / LP;
-        if (r >= heads) return;
-        const bool k = r >= p.side[0].heads;
-        const void *in = k ? p.side[1].in : p.side[0].in;
-        const long long at = (k ? in1 : in0) + r * p.D;
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-            if (E * (c * LP + sub) < p.D) load_raw<IN_BF, E>(v[c], in, at + E * LP * c);
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int sub = lane & (LP - 1);
+    const int hq = p.side[0].heads, heads = hq + p.side[1].heads;
+    // the lane's chunks and its angles' groups of four; where halves are paired, what is not turned is in the
+    // lanes behind the pairs.  Neighbouring lanes have neighbouring chunks (a lane with two of them in a row
+    // writes half sectors: 50 us instead of 31 for 8,191 tokens of 40 heads of 128, bf16).
+    int e0 = E * sub, e1 = e0 + E * LP, a0 = e0 / 2, a1 = e1 / 2;
+    if (!p.interleaved) {
+        const int tail = sub - half / E, tails = (p.D - p.R + 2 * E - 1) / (2 * E);
+        a0 = e0, a1 = e0 + 4;
+        if (tail < 0) e1 = e0 + half;
+        else e0 = tail < tails ? p.R + E * tail : p.D, e1 = e0 + E * tails;
+    }
+    const bool on0 = e0 < p.D, on1 = e1 < p.D, turn0 = e0 < p.R, turn1 = e1 < p.R;
+    auto load = [&](int t, int r, Raw<IN_BF, E> (&v)[2]) {
+        if (t >= tokens || r >= heads) return;
+        const bool k = r >= hq;
+        const long long at = (t0 + t) * p.side[k].in_stride + (k ? r - hq : r) * p.D + e0;
+        if (on0) load_raw<IN_BF, E>(v[0], p.side[k].in, at);
+        if (on1) load_raw<IN_BF, E>(v[1], p.side[k].in, at + (e1 - e0));
     };
-    Raw<IN_BF, E> raw[NC];
-    load(warp * kRows, raw);
-    if (threadIdx.x < half) {
+    // the warp's steps: kRows rows of one token each, every `warps`-th of the CTA's
+    int token = 0, first = (threadIdx.x >> 5) * kRows;
+    auto next = [&](int &t, int &f) {
+        f += warps * kRows;
+        while (f >= p.step_rows && t < tokens) f -= p.step_rows, t++;
+    };
+    if (first >= p.step_rows) first -= warps * kRows, next(token, first);
+    Raw<IN_BF, E> raw[2] = {};
+    load(token, first + lane / LP, raw);
+    for (int j = threadIdx.x; j < tokens * half; j += blockDim.x) {
         // turns = pos * inv_freq / (2 pi), kept modulo one: sincospi takes half-turns
-        const double turns = (double)__ldg(p.positions + t) * (double)__ldg(p.inv_freq + threadIdx.x) *
-                             0.15915494309189533577;
+        const int t = TOKENS == 1 ? 0 : j / half, i = j - t * half;
+        const double turns = (double)__ldg(p.positions + t0 + t) * (double)__ldg(p.inv_freq + i) * 0.15915494309189533577;
         const float frac = (float)(turns - rint(turns));
-        float s, c;
-        sincospif(2.0f * frac, &s, &c);
-        cs[threadIdx.x] = make_float2(c, s);
+        sincospif(2.0f * frac, &sin_of[t][i], &cos_of[t][i]);
     }
     __syncthreads();
-    for (int r0 = warp * kRows; r0 < heads; r0 += (kRopeThreads / 32) * kRows) {
-        const int r = r0 + lane / LP;
-        const bool row = r < heads, k = r >= p.side[0].heads;
-        float v[NC][E];
+    const bool any_weight = p.side[0].weight || p.side[1].weight;
+    const float inv_d = 1.0f / (float)p.D;
+    while (token < tokens) {
+        const int t = token, r = first + lane / LP;
+        const bool row = r < heads, k = r >= hq;
+        float x[2][E];
+        to_floats<IN_BF, E>(raw[0], x[0]);
+        to_floats<IN_BF, E>(raw[1], x[1]);
+        f2 v[2][E / 2];
 #pragma unroll
-        for (int c = 0; c < NC; c++) to_floats<IN_BF, E>(raw[c], v[c]);
-        load(r0 + (kRopeThreads / 32) * kRows, raw);  // the next rows
-        const float *weight = row ? (k ? p.side[1].weight : p.side[0].weight) : nullptr;
+        for (int c = 0; c < 2; c++)
+#pragma unroll
+            for (int i = 0; i < E / 2; i++) v[c][i] = pair2(x[c][2 * i], x[c][2 * i + 1]);
+        next(token, first);
+        load(token, first + lane / LP, raw);  // the next rows
         if (any_weight) {  // a warp may hold rows of both sides: every lane takes part in the sum
-            float sum = 0.0f;
+            f2 sums = pair2(0.0f, 0.0f);
+            if (on0) {
 #pragma unroll
-            for (int c = 0; c < NC; c++) {
-                if (E * (c * LP + sub) >= p.D) continue;
-#pragma unroll
-                for (int i = 0; i < E; i++) sum += v[c][i] * v[c][i];
+                for (int i = 0; i < E / 2; i++) sums = fma2(v[0][i], v[0][i], sums);
             }
+            if (on1) {
+#pragma unroll
+                for (int i = 0; i < E / 2; i++) sums = fma2(v[1][i], v[1][i], sums);
+            }
+            float sum, odd;
+            split2(sums, sum, odd);
+            sum += odd;
 #pragma unroll
             for (int o = LP / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            const float *weight = p.side[k].weight;
             if (weight) {
                 const float inv = rsqrtf(sum * inv_d + p.eps);
 #pragma unroll
-                for (int c = 0; c < NC; c++) {
-                    const int e = E * (c * LP + sub);
-                    if (e >= p.D) continue;
+                for (int c = 0; c < 2; c++) {
+                    if (!(c ? on1 : on0)) continue;
 #pragma unroll
                     for (int i = 0; i < E; i += 4) {
-                        const float4 w = __ldg(reinterpret_cast<const float4 *>(weight + e + i));
-                        v[c][i] *= inv * w.x;
-                        v[c][i + 1] *= inv * w.y;
-                        v[c][i + 2] *= inv * w.z;
-                        v[c][i + 3] *= inv * w.w;
+                        const float4 w = __ldg(reinterpret_cast<const float4 *>(weight + (c ? e1 : e0) + i));
+                        v[c][i / 2] = mul2(v[c][i / 2], mul2(pair2(inv, inv), pair2(w.x, w.y)));
+                        v[c][i / 2 + 1] = mul2(v[c][i / 2 + 1], mul2(pair2(inv, inv), pair2(w.z, w.w)));
                     }
                 }
             }
         }
-        float out[NC][E];
+        f2 co[E / 2], si[E / 2];
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+            const int a = min(i ? a1 : a0, kRopeMaxD / 2 - 4);
+            const float4 c = *reinterpret_cast<const float4 *>(cos_of[t] + a), s = *reinterpret_cast<const float4 *>(sin_of[t] + a);
+            co[i / 2] = pair2(c.x, c.y), co[i / 2 + 1] = pair2(c.z, c.w);
+            si[i / 2] = pair2(s.x, s.y), si[i / 2 + 1] = pair2(s.z, s.w);
+        }
         if (p.interleaved) {
 #pragma unroll
-            for (int c = 0; c < NC; c++) {
-                const int e = E * (c * LP + sub);
+            for (int c = 0; c < 2; c++) {
+                if (!(c ? turn1 : turn0)) continue;
 #pragma unroll
-                for (int i = 0; i < E; i++) out[c][i] = v[c][i];
-                if (e < p.R) {
-#pragma unroll
-                    for (int i = 0; i < E; i += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(cs + (e + i) / 2);  // two (cos, sin)
-                        out[c][i] = v[c][i] * a.x - v[c][i + 1] * a.y;
-                        out[c][i + 1] = v[c][i + 1] * a.x + v[c][i] * a.y;
-                        out[c][i + 2] = v[c][i + 2] * a.z - v[c][i + 3] * a.w;
-                        out[c][i + 3] = v[c][i + 3] * a.z + v[c][i + 2] * a.w;
-                    }
+                for (int i = 0; i < E / 2; i++) {
+                    float a, b, cs[2], sn[2];
+                    split2(v[c][i], a, b);
+                    const int n = c * 4 + i;  // angle
+                    split2(co[n / 2], cs[0], cs[1]);
+                    split2(si[n / 2], sn[0], sn[1]);
+                    v[c][i] = pair2(a * cs[n & 1] - b * sn[n & 1], b * cs[n & 1] + a * sn[n & 1]);
                 }
             }
-        } else {
+        } else if (turn0) {
 #pragma unroll
-            for (int c = 0; c < NC; c++) {
-                const int e = E * (c * LP + sub);
-                const bool turn = e < p.R, low = e < half;
-                // lane index, within the row, of the partner elements
-                const int pl = turn ? (low ? e + half : e - half) / E : sub;
-                const float2 *q = cs + (turn ? (low ? e : e - half) : 0);
-                const float sg = low ? -1.0f : 1.0f;
-#pragma unroll
-                for (int i = 0; i < E; i++) {
-                    float o = __shfl_sync(0xFFFFFFFFu, v[0][i], base + (pl & (LP - 1)));
-                    if (NC == 2) {
-                        const float o1 = __shfl_sync(0xFFFFFFFFu, v[NC - 1][i], base + (pl & (LP - 1)));
-                        if (pl >= LP) o = o1;
-                    }
-                    out[c][i] = turn ? v[c][i] * q[i].x + sg * (o * q[i].y) : v[c][i];
-                }
+            for (int i = 0; i < E / 2; i++) {
+                const f2 a = v[0][i], b = v[1][i];
+                v[0][i] = fma2(a, co[i], mul2(b, mul2(si[i], pair2(-1.0f, -1.0f))));
+                v[1][i] = fma2(b, co[i], mul2(a, si[i]));
             }
         }
         if (row) {
-            void *to = k ? p.side[1].out : p.side[0].out;
-            const long long at = (k ? out1 : out0) + r * p.D;
+            void *to = p.side[k].out;
+            const long long at = (t0 + t) * p.side[k].out_stride + (k ? r - hq : r) * p.D + e0;
 #pragma unroll
-            for (int c = 0; c < NC; c++)
-                if (E * (c * LP + sub) < p.D) store_floats<OUT_BF, E>(to, at + E * LP * c, out[c]);
+            for (int c = 0; c < 2; c++) {
+                if (!(c ? on1 : on0)) continue;
+                float y[E];
+#pragma unroll
+                for (int i = 0; i < E / 2; i++) split2(v[c][i], y[2 * i], y[2 * i + 1]);
+                store_floats<OUT_BF, E>(to, at + (c ? e1 - e0 : 0), y);
+            }
         }
     }
 }
 
-template <bool IN_BF, bool OUT_BF>
-void rope_launch(const RopeParams &p, int64_t T, cudaStream_t stream) {
+template <bool IN_BF, bool OUT_BF, int E, int LP, int TOKENS>
+void rope_start(RopeParams &p, cudaStream_t stream) {
+    constexpr int kRows = 32 / LP, kMaxWarps = kRopeThreads / 32;
+    // a warp's steps, shared out evenly
+    const int steps = (p.side[0].heads + p.side[1].heads + kRows - 1) / kRows;
+    const int turns = (TOKENS * steps + kMaxWarps - 1) / kMaxWarps;
+    p.step_rows = steps * kRows;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)T);
-    cfg.blockDim = dim3(kRopeThreads);
+    cfg.gridDim = dim3((unsigned)((p.T + TOKENS - 1) / TOKENS));
+    cfg.blockDim = dim3(32 * ((TOKENS * steps + turns - 1) / turns));
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (p.R % 16 == 0) {
-        if (p.D <= 32) cudaLaunchKernelEx(&cfg, rope_kernel<IN_BF, OUT_BF, 8, 4, 1>, p);
-        else if (p.D <= 64) cudaLaunchKernelEx(&cfg, rope_kernel<IN_BF, OUT_BF, 8, 8, 1>, p);
-        else if (p.D <= 128) cudaLaunchKernelEx(&cfg, rope_kernel<IN_BF, OUT_BF, 8, 16, 1>, p);
-        else cudaLaunchKernelEx(&cfg, rope_kernel<IN_BF, OUT_BF, 8, 32, 1>, p);
+    cudaLaunchKernelEx(&cfg, rope_kernel<IN_BF, OUT_BF, E, LP, TOKENS>, p);
+}
+
+template <bool IN_BF, bool OUT_BF, int E, int LP>
+void rope_tokens(RopeParams &p, cudaStream_t stream) {
+    // Four tokens a CTA where that fills its waves to four fifths (8,191 tokens of 40 heads of 128: 31.3 us
+    // against 34.3 with one), one token elsewhere (2,600 tokens of 40 heads of 64: 6.2 us against 7.2).
+    const long long ctas = ((long long)p.T + kRopeTokens - 1) / kRopeTokens, slots = (long long)sm_count() * kRopeCtas;
+    if (5 * ctas >= 4 * slots * ((ctas + slots - 1) / slots)) rope_start<IN_BF, OUT_BF, E, LP, kRopeTokens>(p, stream);
+    else rope_start<IN_BF, OUT_BF, E, LP, 1>(p, stream);
+}
+
+template <bool IN_BF, bool OUT_BF>
+void rope_launch(RopeParams &p, cudaStream_t stream) {
+    if (p.interleaved || p.R % 16 == 0) {
+        if (p.D <= 32) rope_tokens<IN_BF, OUT_BF, 8, 2>(p, stream);
+        else if (p.D <= 64) rope_tokens<IN_BF, OUT_BF, 8, 4>(p, stream);
+        else if (p.D <= 128) rope_tokens<IN_BF, OUT_BF, 8, 8>(p, stream);
+        else rope_tokens<IN_BF, OUT_BF, 8, 16>(p, stream);
     } else {
-        if (p.D <= 32) cudaLaunchKernelEx(&cfg, rope_kernel<IN_BF, OUT_BF, 4, 8, 1>, p);
-        else if (p.D <= 128) cudaLaunchKernelEx(&cfg, rope_kernel<IN_BF, OUT_BF, 4, 32, 1>, p);
-        else cudaLaunchKernelEx(&cfg, rope_kernel<IN_BF, OUT_BF, 4, 32, 2>, p);
+        if (p.D <= 32) rope_tokens<IN_BF, OUT_BF, 4, 4>(p, stream);
+        else if (p.D <= 128) rope_tokens<IN_BF, OUT_BF, 4, 16>(p, stream);
+        else rope_tokens<IN_BF, OUT_BF, 4, 32>(p, stream);
     }
 }
 
@@ -281,17 +319,18 @@ extern "C" sherry_status sherry_qk_norm_rope(const sherry_rope *r, sherry_stream
     }
     p.positions = r->positions;
     p.inv_freq = r->inv_freq;
+    p.T = (int)r->T;
     p.D = r->D;
     p.R = r->R;
     p.interleaved = r->interleaved;
     p.eps = r->eps;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (r->in_type == SHERRY_BF16) {
-        if (r->out_type == SHERRY_BF16) rope_launch<true, true>(p, r->T, s);
-        else rope_launch<true, false>(p, r->T, s);
+        if (r->out_type == SHERRY_BF16) rope_launch<true, true>(p, s);
+        else rope_launch<true, false>(p, s);
     } else {
-        if (r->out_type == SHERRY_BF16) rope_launch<false, true>(p, r->T, s);
-        else rope_launch<false, false>(p, r->T, s);
+        if (r->out_type == SHERRY_BF16) rope_launch<false, true>(p, s);
+        else rope_launch<false, false>(p, s);
     }
     return launch_status("sherry_qk_norm_rope");
 }

@@ -99,6 +99,27 @@ def test_rope_odd_head_sizes_and_strides(D, R, inter):
     run_rope(9, 7, 2, D, R, torch.float32, BF, D % 16 == 0, inter, seed=D, pad=16)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,hq,hk,D,R,src,dst,norm", [
+    (2043, 3, 2, 64, 64, torch.float32, BF, True), (2041, 1, 0, 128, 64, BF, BF, True), (2042, 9, 3, 72, 40, BF, torch.float32, False),
+    (1, 80, 9, 128, 128, torch.float32, BF, True), (2040, 17, 1, 16, 8, torch.float32, torch.float32, True),
+    (3, 60, 1, 256, 248, BF, BF, True), (2043, 2, 2, 136, 56, BF, BF, False),
+])
+def test_rope_many_tokens_and_many_heads(T, hq, hk, D, R, src, dst, norm, inter):
+    """About 2,000 tokens go four to a CTA, the last one not full; many heads take a warp several steps."""
+    if hk:
+        run_rope(T, hq, hk, D, R, src, dst, norm, inter, seed=T + D, pad=8)
+    else:   # one side alone, against the same rows as the second side of two
+        x = torch.randn(T, hq, D, device="cuda").to(src)
+        w = torch.rand(D, device="cuda")
+        pos = torch.arange(T, dtype=torch.int32, device="cuda")
+        f = torch.rand(R // 2, device="cuda")
+        q, _ = S.qk_norm_rope(x, None, pos, f, q_weight=w, interleaved=inter, out_dtype=dst)
+        _, k = S.qk_norm_rope(torch.zeros_like(x), x, pos, f, k_weight=w, interleaved=inter, out_dtype=dst)
+        few, _ = S.qk_norm_rope(x[-5:], None, pos[-5:], f, q_weight=w, interleaved=inter, out_dtype=dst)
+        assert torch.equal(q, k) and torch.equal(q[-5:], few)
+
+
 def test_rope_one_side_and_in_place():
     x = torch.randn(4, 6, 64, device="cuda")
     pos = torch.arange(4, dtype=torch.int32, device="cuda")

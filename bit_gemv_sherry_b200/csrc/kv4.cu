@@ -11,22 +11,22 @@ __device__ unsigned int g_kv4_device_error = 0;
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr long long kManySteps = 148 * 64 * 4;  // warp steps of a few waves
+constexpr long long kManySteps = 148 * 128;  // warp steps of a wave or two
 
 struct KvIo {
     void *k, *v;
     long long k_stride, v_stride;
 };
 
-// min and max that keep a NaN
-__device__ __forceinline__ float min_nan(float a, float b) {
+// min and max of three that keep a NaN
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
     float d;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -66,15 +66,25 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
     asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 
 // Smallest and largest element of a row of L lanes.  bf16: both in one register, (min, -max), so that one
 // shuffle a level serves both.
-template <bool BF, int L>
-__device__ __forceinline__ void row_range(const uint4 (&u)[BF ? 1 : 2], const float (&x)[8], float &lo, float &hi) {
+template <bool BF, int L, int C>
+__device__ __forceinline__ void row_range(const uint4 (&u)[C][BF ? 1 : 2], const float (&x)[C][8], float &lo, float &hi) {
     if (BF) {
-        const uint32_t neg = 0x80008000u;
-        const uint32_t a = min2_nan(min2_nan(u[0].x, u[0].y), min2_nan(u[0].z, u[0].w));
-        const uint32_t b = min2_nan(min2_nan(u[0].x ^ neg, u[0].y ^ neg), min2_nan(u[0].z ^ neg, u[0].w ^ neg));
+        uint32_t a = u[0][0].x, b = u[0][0].x;
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            const uint32_t w[4] = {u[c][0].x, u[c][0].y, u[c][0].z, u[c][0].w};
+#pragma unroll
+            for (int i = c ? 0 : 1; i < 4; i++) a = min2_nan(a, w[i]), b = max2_nan(b, w[i]);
+        }
+        b ^= 0x80008000u;
         // (a.lo, b.lo) and (a.hi, b.hi)
         uint32_t m = min2_nan(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
 #pragma unroll
@@ -82,50 +92,55 @@ __device__ __forceinline__ void row_range(const uint4 (&u)[BF ? 1 : 2], const fl
         lo = __uint_as_float(m << 16);
         hi = -__uint_as_float(m & 0xFFFF0000u);
     } else {
-        lo = x[0], hi = x[0];
+        lo = x[0][0], hi = x[0][0];
 #pragma unroll
-        for (int j = 1; j < 8; j++) {
-            lo = min_nan(lo, x[j]);
-            hi = max_nan(hi, x[j]);
-        }
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                lo = min_nan(lo, x[c][j], x[c][j + 1]);
+                hi = max_nan(hi, x[c][j], x[c][j + 1]);
+            }
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-            hi = max_nan(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, lo, o), top = __shfl_xor_sync(0xFFFFFFFFu, hi, o);
+            lo = min_nan(lo, other, other);
+            hi = max_nan(hi, top, top);
         }
     }
 }
 
-// A row of D elements is D / 8 lanes of eight elements, one code word each.  A warp takes up to STEPS
-// times 32 lanes' worth of one token's rows (the key heads, then the value heads): the token's page is
+// A row of D elements is D / (8 C) lanes of C chunks of eight elements, a code word each.  A warp takes up to
+// STEPS times 32 lanes' worth of one token's rows (the key heads, then the value heads): the token's page is
 // looked up once, and all of the warp's loads are under way before the first is used.  One read and one
 // write per element bound it, if the conversions keep to the fast pipes: a code becomes a float, and a
 // float a code, by adding 2^23 or 1.5 2^23 (the conversion instructions run at a quarter of the rate:
-// 32,768 tokens of 8 heads of 128 took 139 us to write and read with them, 82 without; instruction issue,
-// 70 to 80% busy, is what bounds it now, above the 53 us of its bytes).
-template <int D, int STEPS>
-__host__ __device__ constexpr int rows_per_warp() { return STEPS * 32 / (D / 8); }
+// 32,768 tokens of 8 heads of 128, bf16, took 139 us to write and read with them, 82 without, and 62 with four
+// chunks a lane, which share the row's step and addresses; the bytes take 53).
+template <int D, int C, int STEPS>
+__host__ __device__ constexpr int rows_per_warp() { return STEPS * 32 / (D / (8 * C)); }
 
-template <int D, bool BF, bool WRITE, int STEPS>
+template <int D, bool BF, bool WRITE, int C, int STEPS>
 __global__ void __launch_bounds__(kKvThreads)
     kv4_rows_kernel(const __grid_constant__ Kv4View c, const __grid_constant__ KvIo io, unsigned int *err) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int L = D / 8, kRows = rows_per_warp<D, STEPS>();
+    constexpr int L = D / (8 * C), kRows = rows_per_warp<D, C, STEPS>();
     const int lane = threadIdx.x & 31, sub = lane & (L - 1);
     const unsigned parts = (unsigned)(2 * c.H + kRows - 1) / kRows;
     const unsigned w = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
     const int t = (int)(w / parts), row0 = (int)(w % parts) * kRows + lane / L;
     if (t >= c.T) return;
-    // row r: head r of the keys, or head r - H of the values
+    // row r: head r of the keys, or head r - H of the values; chunk k of the lane is elements 8 (sub + k L) ...
     const long long k_at = t * io.k_stride + 8 * sub, v_at = t * io.v_stride - (long long)c.H * D + 8 * sub;
     auto at = [&](int r) { return (r < c.H ? k_at : v_at) + (long long)r * D; };
-    uint4 u[STEPS][BF ? 1 : 2];
+    uint4 u[STEPS][C][BF ? 1 : 2];
     if (WRITE) {
 #pragma unroll
         for (int i = 0; i < STEPS; i++) {
             const int r = row0 + i * (32 / L);
-            if (r < 2 * c.H) load8<BF>(r < c.H ? io.k : io.v, at(r), u[i]);
+            if (r >= 2 * c.H) continue;
+#pragma unroll
+            for (int k = 0; k < C; k++) load8<BF>(r < c.H ? io.k : io.v, at(r) + 8 * L * k, u[i][k]);
         }
     }
     int b = 0, pos = -1, page = -1;
@@ -140,53 +155,60 @@ __global__ void __launch_bounds__(kKvThreads)
         for (int i = 0; i < STEPS; i++) {
             const int r = row0 + i * (32 / L);
             const bool in = r < 2 * c.H;
-            float x[8], lo, hi;
-            floats8<BF>(u[i], x);
-            row_range<BF, L>(u[i], x, lo, hi);  // (lanes past the last row take part with whatever they hold)
+            float x[C][8], lo, hi;
+#pragma unroll
+            for (int k = 0; k < C; k++) floats8<BF>(u[i][k], x[k]);
+            row_range<BF, L, C>(u[i], x, lo, hi);  // (lanes past the last row take part with whatever they hold)
             const uint32_t s16 = __bfloat16_as_ushort(__float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f)));
             const uint32_t m16 = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
             uint32_t pair = s16 | (m16 << 16);
             const float s = kv4_step(pair), m = kv4_low(pair);
             const bool bad = !(fabsf(s) < INFINITY && fabsf(m) < INFINITY);
             const bool flat = s < 7.52316384526264e-37f;  // 2^-120: 1 / s would overflow soon after
-            uint32_t word = 0;
+            uint32_t word[C] = {};
             if (!bad && !flat) {
                 const float inv = __frcp_rn(s);
                 // Every operation is monotone, so the row's ends tell whether any code needs clamping.
-                if (__fmul_rn(__fsub_rn(lo, m), inv) >= -0.5f && __fmul_rn(__fsub_rn(hi, m), inv) < 15.5f) {
+                const bool inside = __fmul_rn(__fsub_rn(lo, m), inv) >= -0.5f && __fmul_rn(__fsub_rn(hi, m), inv) < 15.5f;
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        float a, b;  // 0x4B400000 + rint (the product is not paired: it must be rounded before the sum)
-                        split2(add2(pair2(x[j], x[j + 1]), pair2(-m, -m)), a, b);
-                        split2(add2(pair2(__fmul_rn(a, inv), __fmul_rn(b, inv)), pair2(12582912.0f, 12582912.0f)), a, b);
-                        word += (__float_as_uint(a) << (4 * j)) + (__float_as_uint(b) << (4 * j + 4));
-                    }
-                } else {
+                for (int k = 0; k < C; k++) {
+                    if (inside) {
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        // clamped first: the bounds are whole numbers, so the rounding commutes with them
-                        const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[j], m), inv), 0.0f), 15.0f);
-                        word += __float_as_uint(__fadd_rn(q, 12582912.0f)) << (4 * j);
+                        for (int j = 0; j < 8; j += 2) {
+                            float a, b;  // 0x4B400000 + rint (the product is not paired: it must be rounded before the sum)
+                            split2(add2(pair2(x[k][j], x[k][j + 1]), pair2(-m, -m)), a, b);
+                            split2(add2(pair2(__fmul_rn(a, inv), __fmul_rn(b, inv)), pair2(12582912.0f, 12582912.0f)), a, b);
+                            word[k] += (__float_as_uint(a) << (4 * j)) + (__float_as_uint(b) << (4 * j + 4));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            // clamped first: the bounds are whole numbers, so the rounding commutes with them
+                            const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[k][j], m), inv), 0.0f), 15.0f);
+                            word[k] += __float_as_uint(__fadd_rn(q, 12582912.0f)) << (4 * j);
+                        }
                     }
+                    word[k] -= 0x3F400000u;  // what is left of the eight constants: 0x4B400000 (1 + 16 + 256) modulo 2^32
                 }
-                word -= 0x3F400000u;  // what is left of the eight constants: 0x4B400000 (1 + 16 + 256) modulo 2^32
             }
             if (bad) pair = 0x7FFF7FFFu;        // NaN, NaN
             else if (flat) pair &= 0xFFFF0000u;
             if (in) {
                 uint8_t *blk = block(r);
-                reinterpret_cast<uint32_t *>(blk + slot * Kv4<D>::kRow)[sub] = word;
+#pragma unroll
+                for (int k = 0; k < C; k++) reinterpret_cast<uint32_t *>(blk + slot * Kv4<D>::kRow)[sub + k * L] = word[k];
                 if (sub == 0) reinterpret_cast<uint32_t *>(blk + Kv4<D>::kCodes)[slot] = pair;
             }
         }
     } else {
-        uint32_t word[STEPS], pair[STEPS];
+        uint32_t word[STEPS][C], pair[STEPS];
 #pragma unroll
         for (int i = 0; i < STEPS; i++) {
             const int r = row0 + i * (32 / L);
             if (r >= 2 * c.H) continue;
             const uint8_t *blk = block(r);
-            word[i] = reinterpret_cast<const uint32_t *>(blk + slot * Kv4<D>::kRow)[sub];
+#pragma unroll
+            for (int k = 0; k < C; k++) word[i][k] = reinterpret_cast<const uint32_t *>(blk + slot * Kv4<D>::kRow)[sub + k * L];
             pair[i] = reinterpret_cast<const uint32_t *>(blk + Kv4<D>::kCodes)[slot];
         }
 #pragma unroll
@@ -196,35 +218,38 @@ __global__ void __launch_bounds__(kKvThreads)
             const float s = kv4_step(pair[i]), m = kv4_low(pair[i]);
             // code j stays where it is in its half word: 2^23 + c 16^j, so the step is s 16^-j
             const float sj[4] = {s, s * 0.0625f, s * 0.00390625f, s * 0.000244140625f};
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const uint32_t half = j < 4 ? word[i] : word[i] >> 16;
-                const f2 code = add2(pair2u((half & (15u << (4 * (j & 3)))) | 0x4B000000u, (half & (15u << (4 * (j & 3) + 4))) | 0x4B000000u),
-                                     pair2(-8388608.0f, -8388608.0f));  // exact
-                split2(fma2(pair2(sj[j & 3], sj[(j & 3) + 1]), code, pair2(m, m)), x[j], x[j + 1]);
-            }
             void *base = r < c.H ? io.k : io.v;
-            if (BF) {
-                uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-                    w[j] = *reinterpret_cast<const uint32_t *>(&v);
+            for (int k = 0; k < C; k++) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const uint32_t half = j < 4 ? word[i][k] : word[i][k] >> 16;
+                    const f2 code = add2(pair2u((half & (15u << (4 * (j & 3)))) | 0x4B000000u, (half & (15u << (4 * (j & 3) + 4))) | 0x4B000000u),
+                                         pair2(-8388608.0f, -8388608.0f));  // exact
+                    split2(fma2(pair2(sj[j & 3], sj[(j & 3) + 1]), code, pair2(m, m)), x[j], x[j + 1]);
                 }
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at(r)) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-                float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(base) + at(r));
-                f[0] = make_float4(x[0], x[1], x[2], x[3]);
-                f[1] = make_float4(x[4], x[5], x[6], x[7]);
+                if (BF) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                        w[j] = *reinterpret_cast<const uint32_t *>(&v);
+                    }
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at(r) + 8 * L * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(base) + at(r) + 8 * L * k);
+                    f[0] = make_float4(x[0], x[1], x[2], x[3]);
+                    f[1] = make_float4(x[4], x[5], x[6], x[7]);
+                }
             }
         }
     }
 }
 
-template <int D, bool BF, bool WRITE, int STEPS>
+template <int D, bool BF, bool WRITE, int C, int STEPS>
 void rows_launch_steps(const Kv4View &c, const KvIo &io, unsigned int *err, cudaStream_t stream) {
-    const long long threads = 32LL * c.T * ((2 * c.H + rows_per_warp<D, STEPS>() - 1) / rows_per_warp<D, STEPS>());
+    const long long threads = 32LL * c.T * ((2 * c.H + rows_per_warp<D, C, STEPS>() - 1) / rows_per_warp<D, C, STEPS>());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((threads + kKvThreads - 1) / kKvThreads));
     cfg.blockDim = dim3(kKvThreads);
@@ -234,15 +259,18 @@ void rows_launch_steps(const Kv4View &c, const KvIo &io, unsigned int *err, cuda
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kv4_rows_kernel<D, BF, WRITE, STEPS>, c, io, err);
+    cudaLaunchKernelEx(&cfg, kv4_rows_kernel<D, BF, WRITE, C, STEPS>, c, io, err);
 }
 
 template <int D, bool BF, bool WRITE>
 void rows_launch(const Kv4View &c, const KvIo &io, unsigned int *err, cudaStream_t stream) {
-    // Few rows: one step per warp, for the latency (16 tokens of 8 heads of 64, written and read: 3.5 us
-    // against 5.7); many: four, for the loads under way (32,768 tokens: 82 us).
-    if ((long long)c.T * 2 * c.H * (D / 8) / 32 < kManySteps) rows_launch_steps<D, BF, WRITE, 1>(c, io, err, stream);
-    else rows_launch_steps<D, BF, WRITE, 4>(c, io, err, stream);
+    // Few rows: a chunk per lane and a step per warp, for the latency (16 tokens of 8 heads of 64, written and
+    // read: 3.5 us against 5.7).  Many: two steps for the loads under way, of rows on four lanes in bf16 and
+    // eight in fp32 (a load or store of the warp then has at least 64 bytes in a row): 2,500 tokens of 8 heads
+    // of 128, bf16, 10.1 us against 12.1; 32,768, 62 us against 130 (rows on 16 lanes and four steps 82, on
+    // two lanes 92); fp32, 126 us against 139 (on four lanes 149).
+    if ((long long)c.T * 2 * c.H * (D / 8) / 32 < kManySteps) rows_launch_steps<D, BF, WRITE, 1, 1>(c, io, err, stream);
+    else rows_launch_steps<D, BF, WRITE, BF ? D / 32 : D / 64, 2>(c, io, err, stream);
 }
 
 template <bool WRITE>

@@ -248,6 +248,31 @@ def test_cache_write_and_read(ctx, new, D, H, dtype):
     assert S.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("D,H", [(64, 31), (128, 15)])
+def test_cache_many_rows_as_few(D, H, dtype):
+    """A write and a read of many rows and the same rows sequence by sequence, in parts of a hundred: equal bits."""
+    ctx, new = [733, 1, 0, 640], [700, 1, 5, 640]
+    bt = Batch(ctx, new, H, D, seed=D, extra_rows=2).dev()
+    mag = 10.0 ** torch.randint(-30, 30, (bt.T, H, 1), device="cuda").float()
+    x = [(torch.randn(bt.T, H, D, device="cuda") * mag).to(dtype) for _ in range(2)]
+    x[0][3, 2, 7], x[1][5, 1, 0], x[0][9, 4] = float("nan"), float("inf"), -2.5
+    S.kv4_write(bt.d_cache, x[0], x[1], bt.d_table, bt.d_lens, cu_q=bt.d_cu)
+    k, v = S.kv4_read(bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu, rows=bt.T, dtype=dtype)
+    parts = torch.from_numpy(bt.cache).cuda()
+    for b, (c, n) in enumerate(zip(ctx, new)):
+        for i in range(max(n - c, 0), n, 100):
+            m = min(100, n - i)
+            rows = slice(int(bt.cu[b]) + i, int(bt.cu[b]) + i + m)
+            args = (bt.d_table[b:b + 1], torch.tensor([c - n + i + m], dtype=torch.int32, device="cuda"))
+            cu = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+            S.kv4_write(parts, x[0][rows].contiguous(), x[1][rows].contiguous(), *args, cu_q=cu)
+            pk, pv = S.kv4_read(parts, *args, cu_q=cu, rows=m, dtype=dtype)
+            assert torch.equal(pk.nan_to_num(7.0), k[rows].nan_to_num(7.0)) and torch.equal(pv.nan_to_num(7.0), v[rows].nan_to_num(7.0))
+    assert torch.equal(parts, bt.d_cache) and S.device_error() == 0
+    assert torch.isnan(k[3, 2]).all() and torch.isnan(v[5, 1]).all() and torch.all(k[9, 4] == -2.5)
+
+
 def test_read_makes_its_own_tensors():
     bt = Batch([5, 64], [1, 1], 2, 64, seed=4).fill().dev()
     k, v = S.kv4_read(bt.d_cache, bt.d_table, bt.d_lens)

@@ -805,15 +805,14 @@ sherry_status few_launch(AttnParams p, cudaStream_t stream) {
     using F = Few<D, NT>;
     static OccupancyCache cache;
     const int bps = few_blocks_per_sm(attn_few_kernel<D, NT, 0>, F::kSmem, cache);
-    // at most this many row tiles
-    long long tiles = (long long)p.c.T * p.g / F::kRows + p.c.B;
-    if (p.few_rows < 0x7FFFFFFF)
-        tiles = std::min(tiles, (long long)p.c.B * ((p.few_rows + F::kRows - 1) / F::kRows));
-    if (!p.c.cu) tiles = (long long)p.c.B * ((p.g + F::kRows - 1) / F::kRows);
-    // and with the rows shared out evenly this many
-    const long long even = std::min(tiles, ((long long)p.c.T * p.g / p.c.B + F::kRows - 1) / F::kRows * p.c.B) * p.c.H;
+    // at most this many row tiles, and with the rows shared out evenly so many
+    const long long seqs = std::min(p.c.B, p.c.T), rows = (long long)p.c.T * p.g;  // sequences with rows, at most
+    long long tiles = rows / F::kRows + seqs;
+    if (p.few_rows < 0x7FFFFFFF) tiles = std::min(tiles, seqs * ((p.few_rows + F::kRows - 1) / F::kRows));
+    if (!p.c.cu) tiles = seqs * ((p.g + F::kRows - 1) / F::kRows);
+    const long long even = std::min(tiles, (rows + seqs * F::kRows - 1) / (seqs * F::kRows) * seqs) * p.c.H;
     tiles *= p.c.H;
-    if (tiles > 0x7FFFFFFF / 8) return SHERRY_ERR_UNSUPPORTED;
+    if (tiles > 0x7FFFFFFF) return SHERRY_ERR_UNSUPPORTED;
     // A cluster per row tile, or equal runs and a join.  In pages one after the other, if every sequence is as
     // long as its table: the largest cluster of which all are resident at once, against the runs and about
     // kJoinPages for the join and its launch.  Clusters and runs, us, one new token and 8 heads each: one

@@ -369,6 +369,15 @@ def test_attn_in_runs(ctx, new, hq, H, D):
     assert torch.allclose(out[:rows].float(), short[:rows].float(), rtol=2.0 ** -7, atol=2.0 ** -10 * short[:rows].abs().max().item())
 
 
+@pytest.mark.parametrize("wide", [0, WIDE])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("some", [[1, 1, 2], [5, 1, 3], [40, 2, 1]])
+def test_attn_most_sequences_have_no_new_token(some, D, wide):
+    new, ctx = [0] * 150, [i % 90 for i in range(150)]
+    new[3], new[77], new[149] = some
+    bt, q, out = run_attn(ctx, new, 8, 2, D, seed=D, extra=2, wide=wide)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n,new,hq,H", [(5, 1, 32, 8), (11, 1, 32, 8), (24, 1, 8, 8), (50, 1, 8, 8), (90, 1, 16, 8), (13, 5, 32, 8), (26, 3, 32, 8),
                                         (45, 3, 32, 8)])

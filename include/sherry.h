@@ -513,6 +513,7 @@ sherry_status sherry_qk_norm_rope(const sherry_rope *r, sherry_stream_t stream);
  *   page_table  [B][table_stride] int32, the first `width` of a row used: position p
  *               of sequence b is in slot p % 64 of page page_table[b][p / 64].
  *               Entries past a sequence's length are not read.
+ *               (For a few short sequences a `width` near their pages in use is faster: it picks kernels.)
  *   ctx_lens    [B] int32, tokens of each sequence, the new ones included.
  *   cu_q        [B + 1] int32, ascending: rows cu_q[b] .. cu_q[b + 1] - 1 of the ragged
  *               tensors are the last positions of sequence b.  NULL: B = T, one each.

@@ -565,6 +565,20 @@ def test_waits_that_run_out_are_reported(new):
     assert torch.equal(S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu), out)
 
 
+def test_waits_that_run_out_in_runs_are_reported():
+    bt, q, out = run_attn([700, 690], [1, 1], 32, 8, 64, seed=38, wide=WIDE)
+    dq = torch.from_numpy(q).cuda().bfloat16()
+    S.set_wait_limit(16)
+    try:
+        for _ in range(2):
+            S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens)
+        assert S.device_error() in (0, 6)
+    finally:
+        S.set_wait_limit(0)
+    assert S.device_error() == 0
+    assert torch.equal(S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens), out)
+
+
 @pytest.mark.parametrize("new", [[1], [140]])
 def test_attn_peaked_scores_and_large_values(new):
     run_attn([333], new, 4, 2, 64, seed=5, qmag=30.0)

@@ -6,9 +6,10 @@ Tolerances, from the arithmetic (u = 2^-24, a rounding to bf16 at most 2^-8 rela
 rotation  cos and sin: the fraction of a turn is rounded once (2^-26 turns = 2 pi 2^-26 rad <
           2^-23.3) and sincospi is within 2 ulp (2^-23): below 2^-22 in all.  The two products
           and the sum round three times, (|a| + |b|) 3 u.  Together (|a| + |b|) 2^-21.3; taken
-          as 2^-21.  With a norm the sum of squares (at most 8 additions deep: 2 per lane, 5
-          shuffles, and a rounding per square), the mean, the sum with eps, the root, the
-          quotient and two products add at most 16 u relative: 2^-20, in all (|a| + |b|) 2^-19.
+          as 2^-21.  With a norm a term of the sum of squares passes at most 14 roundings (8 in a lane,
+          one to join its two sums, 5 shuffles), which the root halves to 7 u; the mean and the sum with
+          eps add 1 u, the reciprocal root 4 u (2 ulp), two products 2 u: below 16 u relative, 2^-20, in
+          all (|a| + |b|) 2^-19.
 cache     codes, steps and low ends are equal bit for bit (one rounding after another, in the
           same order); read back, fl32(m + s c) is exact and bf16 rounds that once more.
 attention few rows: x_t = scale * q.k_t is summed in fp32 on codes 0 .. 15: D / 8 sums of 16 products,

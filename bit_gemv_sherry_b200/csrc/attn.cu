@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "attn.cuh"
+#include "page_ring.h"
 
 namespace sherry {
 namespace {
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
         walk.start(p, work, from, to);
     }
 
-    int copied = 0, to_copy = 0;
+    PageRing<kS> pages;
     if (lane == 0) {
         ahead = walk;
         ahead_page = walk.page0;
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             ahead_page = ahead.page0;
             if (ahead.s.len > p.c.width * SHERRY_KV4_PAGE) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
         }
-        const int s = to_copy;
+        const int s = pages.to;
         const int page = ahead.s.len > 0 ? kv4_page(p.c, ahead.b, ahead_page * SHERRY_KV4_PAGE, p.err) : -1;
         there[s] = page >= 0;
         if (page >= 0) {
@@ -271,8 +272,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             mbar_arrive(full + s);
         }
         ahead_page += kStep;
-        copied++;
-        to_copy = to_copy + 1 == kS ? 0 : to_copy + 1;
+        pages.copy();
     };
     if (lane == 0)
         for (int s = 0; s < kS; s++) copy_next();
@@ -284,9 +284,13 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
     const int tok_r = r ^ (r >> 2 & 1);                       // rows r and r + 8 (+ 8)
     const int tok_v0 = (2 * c) ^ (c >> 1 & 1), tok_v1 = (2 * c + 1) ^ (c >> 1 & 1);
     const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;  // a negative scale turns q's signs
-    int it = 0, s = 0;        // pages done, ring slot of the next
-    uint32_t lap = 0;         // its phase
-    bool dead = false;
+    // After a wait that ran out: copies in flight land before their memory is used again or released.
+    auto drain = [&]() {
+        volatile int no_abort = 0;
+        if (lane == 0)
+            pages.drain([&](int s, uint32_t phase) { mbar_wait(full + s, phase, &no_abort, p.err, 1000000000LL); });
+        __syncwarp();
+    };
     for (bool more = CL || walk.next(p); more; more = !CL && walk.next(p)) {
         const int nrow = walk.s.rows * p.g, row0 = walk.tile * kRows;
         const int pos0 = walk.s.len - walk.s.rows;            // position of the first new token
@@ -362,10 +366,11 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
 #pragma unroll
             for (int j = 0; j < 2; j++) m[t][j] = -INFINITY, ref[t][j] = 0.0f, l[t][j] = 0.0f, corr[t][j] = 0.0f;
         }
-        for (int pg = walk.page0; pg < walk.page1; pg += kStep, it++) {
-            dead = dead || !__all_sync(0xFFFFFFFFu, mbar_wait(full + s, lap, abort, p.err, p.wait_limit));
+        for (int pg = walk.page0; pg < walk.page1; pg += kStep) {
+            const int s = pages.at;
+            if (!pages.dead) pages.take(__all_sync(0xFFFFFFFFu, mbar_wait(full + s, pages.lap, abort, p.err, p.wait_limit)));
             const int t0 = pg * SHERRY_KV4_PAGE;              // first token of the page
-            if (!dead && there[s] && t0 <= last_max) {
+            if (!pages.dead && there[s] && t0 <= last_max) {
                 const uint8_t *kb = ring + s * F::kStage, *vb = kb + Kv4<D>::kBlock;
                 const bool whole = t0 + SHERRY_KV4_PAGE - 1 <= last_min;
                 const uint32_t a1[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
@@ -559,8 +564,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                     }
             }
             __syncwarp();
-            if (lane == 0 && !dead) copy_next();
-            if (++s == kS) s = 0, lap ^= 1;
+            if (lane == 0 && !pages.dead) copy_next();
         }
 
         // ---------------- the piece's result ----------------
@@ -581,13 +585,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                 }
             }
         if (CL) {
-            if (dead && lane == 0) {
-                // copies in flight land before their memory is used again
-                volatile int no_abort = 0;
-                for (int j = max(it, copied - kS); j < copied; j++)
-                    mbar_wait(full + j % kS, (j / kS) & 1, &no_abort, p.err, 1000000000LL);
-            }
-            __syncwarp();
+            if (pages.dead) drain();
             // each warp's part into its own ring: [row][D] sums, then the rows' references and totals
             float *part = reinterpret_cast<float *>(ring);
 #pragma unroll
@@ -670,12 +668,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                 }
             }
     }
-    if (dead && lane == 0) {
-        // copies in flight land before the CTA's shared memory is released
-        volatile int no_abort = 0;
-        for (int j = max(it, copied - kS); j < copied; j++)
-            mbar_wait(full + j % kS, (j / kS) & 1, &no_abort, p.err, 1000000000LL);
-    }
+    if (pages.dead) drain();
 }
 
 // Joins the parts of the row tiles that the runs cut: a CTA per 8 rows of one, JW warps per row, which take

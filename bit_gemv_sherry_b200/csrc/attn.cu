@@ -291,6 +291,10 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             pages.drain([&](int s, uint32_t phase) { mbar_wait(full + s, phase, &no_abort, p.err, 1000000000LL); });
         __syncwarp();
     };
+    if (p.wait_limit == 1) {  // a drill: no wait is given a look, with the first copies on their way
+        pages.dead = true;
+        if (lane == 0) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_TIMEOUT);
+    }
     for (bool more = CL || walk.next(p); more; more = !CL && walk.next(p)) {
         const int nrow = walk.s.rows * p.g, row0 = walk.tile * kRows;
         const int pos0 = walk.s.len - walk.s.rows;            // position of the first new token

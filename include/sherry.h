@@ -595,8 +595,9 @@ sherry_status sherry_device_error(void);
 /*
  * sherry_set_wait_limit -- limit, in SM clock cycles, of the bounded waits of
  * kernels launched after this call by any thread of the process (the GEMM's
- * operand and accumulator barriers, the attention's copies and products).  0 restores the default of 4e9 cycles
- * (about 2 s at 1.9 GHz).  Meant for tests and failure drills: with a small
+ * operand and accumulator barriers, the attention's copies and products).  0 restores the
+ * default of 4e9 cycles (about 2 s at 1.9 GHz).  With a limit of 1 the attention's waits for
+ * pages of few new tokens give up without a look (a longer one may find its page there).  Meant for tests and failure drills: with a small
  * limit the waits give up, the kernel records SHERRY_ERR_TIMEOUT (read and
  * cleared by sherry_device_error), lets the copies and MMAs it already issued
  * finish (those drains keep their own long limit), releases its tensor memory

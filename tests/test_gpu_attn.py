@@ -580,6 +580,30 @@ def test_waits_that_run_out_in_runs_are_reported():
     assert torch.equal(S.attn_kv4(dq, bt.d_cache, bt.d_table, bt.d_lens), out)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx,new,wide", [
+    ([700, 690], 1, 0), ([700, 690], 1, WIDE),           # a cluster per row tile; runs and a join
+    ([700, 690, 64, 0], 3, 0), ([700, 690, 64, 0], 3, WIDE), ([40], 1, 0), ([9000], 1, WIDE),
+])
+def test_waits_without_a_look_are_reported_and_leave_no_copy_behind(ctx, new, wide, D):
+    """With a limit of 1 no wait is given a look while a ring of copies is on its way: the status is the
+    timeout's, the next calls' shared memory is their own, and they are exact."""
+    bt, q, out = run_attn(ctx, [new] * len(ctx), 32, 8, D, seed=39, wide=wide, max_q=new)
+    dq = torch.from_numpy(q).cuda().bfloat16()
+    args = (dq, bt.d_cache, bt.d_table, bt.d_lens)
+    again = []
+    for _ in range(3):
+        S.set_wait_limit(1)
+        try:
+            S.attn_kv4(*args, cu_q=bt.d_cu, max_q=new)
+        finally:
+            S.set_wait_limit(0)
+        # right behind it, with no look at the status between
+        again += [S.attn_kv4(*args, cu_q=bt.d_cu, max_q=new) for _ in range(3)]
+        assert S.device_error() == 6 and S.device_error() == 0
+    assert all(torch.equal(o, out) for o in again)
+
+
 @pytest.mark.parametrize("new", [[1], [140]])
 def test_attn_peaked_scores_and_large_values(new):
     run_attn([333], new, 4, 2, 64, seed=5, qmag=30.0)

@@ -182,11 +182,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return d;
 }
 
-// A probability of 1 times the largest step is held as about 2^kUp: fp16 has room for references that lag
-// by 2^8, and 2^-21 of the largest still has its 11 bits.
-constexpr float kUp = 7.0f;
-
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+// The softmax's state, for each row: with x a score in powers of two,
+//     p = 2^(x - ref),   l = sum p,   corr = sum p (m + 8 s),   o = sum fp16(p s 2^-ve) c.
+// ref is a whole number, kDown above the largest score when it was set; it moves when p passes 2^-8, so that
+// the weights of 65,536 equal tokens sum to no more than 2^8 and l and corr stay in fp32's range for any value.
+// ve follows the largest p s that the row met, not the largest s: tokens that the row does not see, or that have
+// no weight in it, cost the others nothing (one power for all rows and tokens, and one reference for l and o,
+// gave inf for a constant value row of 2^22 and zeros beside an unseen value of 1e30).  The largest p s 2^-ve is
+// 2^kUp when ve is set: fp16 has room for it to grow by 2^8 before ve moves, and 2^-21 of it still has its 11
+// bits.  Moves are by whole powers of two, so no sum is rounded by them.
+constexpr int kUp = 7, kDown = 16;
+constexpr float kPTop = 0.00390625f;  // four of a lane's p sum up to more: ref has to move
+constexpr float kPsTop = 32768.0f;    // four of a lane's p s 2^-ve sum up to more: ve has to move
+constexpr float kNoRef = -1e38f;      // before the first score: any score passes it, and unseen tokens (-inf) do not
 
 // CL > 0: a cluster of CL CTAs takes one row tile, its warps every 4 CL-th page each, and their parts meet
 // through distributed shared memory: no second kernel.  For few row tiles of few pages (see few_launch).
@@ -301,7 +309,8 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
         // q: lane (r, c) holds elements [c D / 4, (c + 1) D / 4) of row r of each row group
         // as fp16 of q 2^-e, the odd nibbles' elements 2^-4 of it again
         uint32_t qf[NT][MT][2];
-        float qsum[NT][2], sc[NT][2];                         // of rows 2 c, 2 c + 1: sum(q), scale of a score
+        float qsum[NT][2];                                    // of rows 2 c, 2 c + 1: sum(q),
+        f2 sc[NT];                                            // scale of a score
         int last[NT][2];                                      // last token those rows see
 #pragma unroll
         for (int t = 0; t < NT; t++) {
@@ -343,32 +352,31 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                 }
             }
             sum *= d0 * 5.9604644775390625e-08f;              // 2^-24: in units of the product
+            float scale[2];
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 qsum[t][j] = __shfl_sync(0xFFFFFFFFu, sum, (2 * c + j) * 4);
                 // (not 0: a score of -inf has to stay one)
-                sc[t][j] = fmaxf(fabsf(p.scale2) * pow2(24 + __shfl_sync(0xFFFFFFFFu, e, (2 * c + j) * 4)), 1e-37f);
+                scale[j] = fmaxf(fabsf(p.scale2) * pow2(24 + __shfl_sync(0xFFFFFFFFu, e, (2 * c + j) * 4)), 1e-37f);
                 const int rw = row0 + 8 * t + 2 * c + j;
                 last[t][j] = rw < nrow ? pos0 + rw / p.g : -1;
             }
+            sc[t] = pair2(scale[0], scale[1]);
         }
         const int hi_row = min(row0 + kRows, nrow) - 1;
         // rows past the end see nothing; their sums are dropped, so they need no mask
         const int last_min = pos0 + row0 / p.g, last_max = pos0 + hi_row / p.g;
-        // All sums are of 2^(x - m) 2^(kUp - ve): m is the row's reference (x in units before the scale), ve
-        // a power of two above the values' steps, and ref = m sc - (kUp - ve).
         float o[NT][MT][4];
-        float m[NT][2], ref[NT][2], l[NT][2], corr[NT][2];
-        int ve = -100;
-        float step_top = pow2(ve), sum_top = pow2(15 - ve);   // a step, a sum of probabilities above it moves them
+        f2 nref[NT], down[NT], l[NT], corr[NT];               // of rows 2 c, 2 c + 1: -ref, 2^-ve, ...
 #pragma unroll
         for (int t = 0; t < NT; t++) {
 #pragma unroll
             for (int i = 0; i < MT; i++)
 #pragma unroll
                 for (int j = 0; j < 4; j++) o[t][i][j] = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 2; j++) m[t][j] = -INFINITY, ref[t][j] = 0.0f, l[t][j] = 0.0f, corr[t][j] = 0.0f;
+            nref[t] = pair2(-kNoRef, -kNoRef);
+            down[t] = pair2(pow2(126), pow2(126));
+            l[t] = corr[t] = pair2(0.0f, 0.0f);
         }
         for (int pg = walk.page0; pg < walk.page1; pg += kStep) {
             const int s = pages.at;
@@ -450,78 +458,90 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                                 }
                         }
                 }
-                float step = fmaxf(sv[0][0], sv[0][1]);
-#pragma unroll
-                for (int qi = 1; qi < kTiles; qi++) step = fmaxf(step, fmaxf(sv[qi][0], sv[qi][1]));
                 uint32_t pb[kTiles][NT][2];
-                float sum[NT][2], csum[NT][2];
-                // The references follow the maximum only when probabilities grow out of fp16: most pages skip the
-                // shuffles and the rescaling.
+                f2 sum[NT], csum[NT];
+                // References and powers move only when a lane's sums outgrow them: most pages skip the shuffles and
+                // the rescaling.
                 for (bool moved = false;; moved = true) {
-                    bool grow = step > step_top;
+                    f2 most[NT];
 #pragma unroll
-                    for (int t = 0; t < NT; t++)
-#pragma unroll
-                        for (int j = 0; j < 2; j++) sum[t][j] = csum[t][j] = 0.0f;
+                    for (int t = 0; t < NT; t++) sum[t] = csum[t] = most[t] = pair2(0.0f, 0.0f);
 #pragma unroll
                     for (int qi = 0; qi < kTiles; qi++)
 #pragma unroll
-                        for (int t = 0; t < NT; t++)
+                        for (int i = 0; i < 2; i++) {
+                            const f2 s2 = pair2(sv[qi][i], sv[qi][i]), m2 = pair2(mv[qi][i], mv[qi][i]);
 #pragma unroll
-                            for (int i = 0; i < 2; i++) {
-                                float ps[2];
-#pragma unroll
-                                for (int j = 0; j < 2; j++) {
-                                    const float pr = exp2_fast(x[qi][t][2 * i + j] * sc[t][j] - ref[t][j]);
-                                    ps[j] = pr * sv[qi][i];
-                                    sum[t][j] += pr;
-                                    csum[t][j] += pr * mv[qi][i];
-                                }
-                                pb[qi][t][i] = pack_f16(ps[0], ps[1]);
-                            }
-#pragma unroll
-                    for (int t = 0; t < NT; t++)
-#pragma unroll
-                        for (int j = 0; j < 2; j++)
-                            grow |= sum[t][j] > sum_top || (m[t][j] == -INFINITY && (whole || t0 + 16 * q0 <= last[t][j]));
-                    // once is enough (a row of nothing but NaN has no reference after it either)
-                    if (moved || !__any_sync(0xFFFFFFFFu, grow)) break;
-                    const int old = ve;
-                    const float most = step < INFINITY ? fmaxf(step, 0.0f) : 0.0f;
-                    ve = max(ve, min((int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)) >> 23) - 126, 100));
-                    step_top = pow2(ve);
-                    sum_top = pow2(15 - ve);
-#pragma unroll
-                    for (int t = 0; t < NT; t++)
-#pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            float mx = x[0][t][j];
-#pragma unroll
-                            for (int k = 1; k < 2 * kTiles; k++) mx = fmaxf(mx, x[k >> 1][t][2 * (k & 1) + j]);
-                            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-                            mx = fmaxf(mx, m[t][j]);
-                            const float f = m[t][j] == -INFINITY ? 0.0f : exp2_fast((m[t][j] - mx) * sc[t][j] + (float)(old - ve));
-                            m[t][j] = mx;
-                            ref[t][j] = (mx == -INFINITY ? 0.0f : mx * sc[t][j]) - (kUp - (float)ve);
-                            l[t][j] *= f;
-                            corr[t][j] *= f;
-                            ones[t][j] *= f;
-#pragma unroll
-                            for (int i = 0; i < MT; i++) {
-                                o[t][i][j] *= f;
-                                o[t][i][2 + j] *= f;
+                            for (int t = 0; t < NT; t++) {
+                                float a, b;
+                                split2(fma2(pair2(x[qi][t][2 * i], x[qi][t][2 * i + 1]), sc[t], nref[t]), a, b);
+                                const f2 pr = pair2(exp2_fast(a), exp2_fast(b));
+                                const f2 ps = mul2(mul2(pr, s2), down[t]);
+                                sum[t] = add2(sum[t], pr);
+                                csum[t] = fma2(pr, m2, csum[t]);
+                                most[t] = add2(most[t], ps);
+                                split2(ps, a, b);
+                                pb[qi][t][i] = pack_f16(a, b);
                             }
                         }
+                    bool grow = false;
+#pragma unroll
+                    for (int t = 0; t < NT; t++) {
+                        float a, b;
+                        split2(sum[t], a, b);
+                        grow |= fmaxf(a, b) > kPTop;
+                        split2(most[t], a, b);
+                        grow |= fmaxf(a, b) > kPsTop;
+                    }
+                    // once is enough (a row of nothing but NaN has no reference after it either)
+                    if (moved || !__any_sync(0xFFFFFFFFu, grow)) break;
+#pragma unroll
+                    for (int t = 0; t < NT; t++) {
+                        float scale[2], old[2], d[2], f[2], fo[2];
+                        split2(sc[t], scale[0], scale[1]);
+                        split2(nref[t], old[0], old[1]);
+                        split2(down[t], d[0], d[1]);
+#pragma unroll
+                        for (int j = 0; j < 2; j++) {
+                            // largest score, and largest score of p s (up to a factor of two)
+                            float mx = -INFINITY, ms = -INFINITY;
+#pragma unroll
+                            for (int k = 0; k < 2 * kTiles; k++) {
+                                const float y = x[k >> 1][t][2 * (k & 1) + j] * scale[j];
+                                mx = fmaxf(mx, y);
+                                ms = fmaxf(ms, y + (float)((int)(__float_as_uint(sv[k >> 1][k & 1]) >> 23 & 255) - 126));
+                            }
+#pragma unroll
+                            for (int k = 4; k < 32; k <<= 1) {
+                                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
+                                ms = fmaxf(ms, __shfl_xor_sync(0xFFFFFFFFu, ms, k));
+                            }
+                            const float ref = fmaxf(-old[j], ceilf(mx) + (float)kDown), by = -old[j] - ref;   // by <= 0
+                            // what is summed already needs no more than its power, by lower
+                            const float ve = (float)(127 - (int)(__float_as_uint(d[j]) >> 23));
+                            const float to = fmaxf(fmaxf(ve + by, ceilf(ms - ref) - (float)kUp), -126.0f);
+                            old[j] = -ref;
+                            d[j] = __int_as_float((127 - (int)to) << 23);
+                            f[j] = exp2_fast(by);
+                            fo[j] = exp2_fast(ve + by - to);
+                            ones[t][j] *= fo[j];
+#pragma unroll
+                            for (int i = 0; i < MT; i++) {
+                                o[t][i][j] *= fo[j];
+                                o[t][i][2 + j] *= fo[j];
+                            }
+                        }
+                        nref[t] = pair2(old[0], old[1]);
+                        down[t] = pair2(d[0], d[1]);
+                        l[t] = mul2(l[t], pair2(f[0], f[1]));
+                        corr[t] = mul2(corr[t], pair2(f[0], f[1]));
+                    }
                 }
 #pragma unroll
-                for (int t = 0; t < NT; t++)
-#pragma unroll
-                    for (int j = 0; j < 2; j++) {
-                        l[t][j] += sum[t][j];
-                        corr[t][j] += csum[t][j];
-                    }
+                for (int t = 0; t < NT; t++) {
+                    l[t] = add2(l[t], sum[t]);
+                    corr[t] = add2(corr[t], csum[t]);
+                }
 #pragma unroll
                 for (int qi = 0; qi < kTiles; qi++) {
                     const int q = q0 + qi;
@@ -571,23 +591,32 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             if (lane == 0 && !pages.dead) copy_next();
         }
 
-        // ---------------- the piece's result ----------------
+        // ---------------- the piece's result: references, totals, sums p v ----------------
+        float ref[NT][2], tot[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; t++)
+        for (int t = 0; t < NT; t++) {
+            float add[2], d[2];
+            split2(nref[t], ref[t][0], ref[t][1]);
+            split2(l[t], tot[t][0], tot[t][1]);
+            split2(corr[t], add[0], add[1]);
+            split2(down[t], d[0], d[1]);
 #pragma unroll
             for (int j = 0; j < 2; j++) {
+                ref[t][j] = -ref[t][j];
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1) {
-                    l[t][j] += __shfl_xor_sync(0xFFFFFFFFu, l[t][j], k);
-                    corr[t][j] += __shfl_xor_sync(0xFFFFFFFFu, corr[t][j], k);
+                    tot[t][j] += __shfl_xor_sync(0xFFFFFFFFu, tot[t][j], k);
+                    add[j] += __shfl_xor_sync(0xFFFFFFFFu, add[j], k);
                 }
+                const float up = __uint_as_float((254u << 23) - __float_as_uint(d[j]));  // 2^ve
 #pragma unroll
                 for (int i = 0; i < MT; i++) {
                     const float f = i & 1 ? 1048576.0f : 16777216.0f;  // the codes' 2^-20 and 2^-24
-                    o[t][i][j] = o[t][i][j] * f + corr[t][j];
-                    o[t][i][2 + j] = o[t][i][2 + j] * f + corr[t][j];
+                    o[t][i][j] = o[t][i][j] * f * up + add[j];
+                    o[t][i][2 + j] = o[t][i][2 + j] * f * up + add[j];
                 }
             }
+        }
         if (CL) {
             if (pages.dead) drain();
             // each warp's part into its own ring: [row][D] sums, then the rows' references and totals
@@ -606,7 +635,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                                             o[t][i + 3][2 * k + j]);
                     if (r == 0)
                         reinterpret_cast<float2 *>(part + kRows * D)[row] =
-                            make_float2(m[t][j] == -INFINITY ? -INFINITY : ref[t][j], l[t][j]);
+                            make_float2(ref[t][j], tot[t][j]);
                 }
             cluster_sync();
             // the cluster's CTAs share the rows; lane i holds the weight of part i, the parts in order
@@ -621,8 +650,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                 float mx = pm;
 #pragma unroll
                 for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
-                // a part without keys has sum 0; a NaN among its scores shows in the sum
-                const float f = pm == -INFINITY ? (pl == 0.0f ? 0.0f : pl) : exp2_fast(pm - mx);
+                const float f = exp2_fast(pm - mx);  // (a part without keys has kNoRef and sums of 0)
                 float sum = lane < kParts ? pl * f : 0.0f, acc = 0.0f;
 #pragma unroll
                 for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
@@ -646,7 +674,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                 const int row = 8 * t + 2 * c + j, rw = row0 + row;
                 if (rw >= nrow) continue;
                 if (all) {
-                    const float inv = l[t][j] == 0.0f ? 0.0f : 1.0f / l[t][j];
+                    const float inv = tot[t][j] == 0.0f ? 0.0f : 1.0f / tot[t][j];
                     uint16_t *dst = p.out + (long long)(walk.s.first + rw / p.g) * p.out_stride +
                                     (long long)(walk.h * p.g + rw % p.g) * D + r * (D / 8);
 #pragma unroll
@@ -668,7 +696,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                                             o[t][i + 3][2 * k + j]);
                     if (r == 0)
                         reinterpret_cast<float2 *>(p.ws + 2LL * p.grid * kRows * D)[slot * kRows + row] =
-                            make_float2(m[t][j] == -INFINITY ? -INFINITY : ref[t][j], l[t][j]);
+                            make_float2(ref[t][j], tot[t][j]);
                 }
             }
     }
@@ -717,8 +745,7 @@ __global__ void __launch_bounds__(256 * JW, JW == 1 ? 2 : 1) attn_join_kernel(co
         float f = 0.0f;
         if (i <= i1) {
             const float2 v = ml[(2LL * i + (i == i0)) * kRows + row];
-            // a part without keys has sum 0; a NaN among its scores shows in the sum
-            f = v.x == -INFINITY ? (v.y == 0.0f ? 0.0f : v.y) : exp2_fast(v.x - m);
+            f = exp2_fast(v.x - m);  // (a part without keys has kNoRef and sums of 0)
             l += v.y * f;
         }
         const int k1 = min(32, i1 - ib + 1);

@@ -38,6 +38,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// 2^e for any e (0 or the largest power where that is out of range).
+__device__ __forceinline__ float pow2(int e) {
+    return e < -126 ? (e < -149 ? 0.0f : __int_as_float(1 << (e + 149))) : __int_as_float((min(e, 127) + 127) << 23);
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));

@@ -102,11 +102,6 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                    "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// 2^e for any e (0 or the largest power where that is out of range).
-__device__ __forceinline__ float pow2(int e) {
-    return e < -126 ? (e < -149 ? 0.0f : __int_as_float(1 << (e + 149))) : __int_as_float((min(e, 127) + 127) << 23);
-}
-
 // Power of two to divide by so that magnitudes up to `most` become at most 2^(bits + 1).
 __device__ __forceinline__ int exp_for(float most, int bits) {
     return max((int)(__float_as_uint(most) >> 23) - 127 - bits, -100);  // most >= 0 and finite

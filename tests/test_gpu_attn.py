@@ -25,6 +25,21 @@ attention few rows: x_t = scale * q.k_t is summed in fp32 on codes 0 .. 15: D / 
           takes 2^-8 * 8 max s_v + 2^-12 max|v| for the roundings of p and v: 2^-5 max s_v is above
           2^-11 * 15 max s_v, and, where a row of values has both signs (max|v| <= 15 max s_v), above the
           tiles' 2^-10 max|v| too.  The last rounding is 2^-8 |o|.
+
+          The bound above takes the largest value of a whole sequence, seen or not.  row_bound counts what a
+          row sees, each token with its probability p: with |v| and |k| a token's largest magnitudes,
+              |do| <= sum p_t (2 |dx_t| + 2^-20 + L 2^-23) (|v_t| + |o|)   weights, in numerator and total
+                      + sum p_t dv_t + L 2^-26 max p_t |v_t| + 2^-8 |o|.
+          A weight is off by a factor within e^+-|dx| and the exponential's 2^-21; fp32 sums of L terms by
+          L 2^-24, the tensor cores' truncated ones by twice that.
+          few rows: |dx_t| as above with the token's own s and m; p s to fp16 is 2^-11 of it, times |c - 8| <= 8,
+          and truncated sums of 16-token products with codes up to 15 (and 8 for the centre): dv_t =
+          s_t (2^-11 8 + L / 16 2^-23 23).
+          tiles: a key's or value's low end and the sum m + s c are each rounded to fp16, half a step of 2^-11
+          each, or 2^-25 of units in which the largest of the token is at least 2^-14: 2^-10 of |k| or |v| in
+          all; probabilities 2^-11: |dx_t| += |scale| sum|q| |k_t| 2^-10, dv_t = |v_t| (2^-10 + 2^-11).
+          Products p s (p v) that are below fp16's normal range are off by 2^-25 where the row's largest is at
+          least 2^6 (2^-4, in the tiles' units): at most 2^-26 of the largest for each token.
 """
 import ctypes
 
@@ -184,6 +199,21 @@ class Batch:
             self.kv.append(vals)
         return self
 
+    def put(self, b, kv, h, t, x):
+        """Row x float32 [D] coded as key (kv 0) or value (1) of token t of sequence b, head h."""
+        codes, s, m = (a[0] for a in A.kv4_encode(x[None]))
+        A.kv4_pack(self.cache, self.table[b, t // 64], t % 64, h, kv, codes, s, m)
+        vals, ss, ms = self.kv[b][kv]
+        vals[h, t], ss[h, t], ms[h, t] = A.kv4_values(codes, s, m), s, m
+
+    def times(self, b, kv, h, t, f):
+        """That row's step and low end times f."""
+        codes, s, m = A.kv4_unpack(self.cache, self.table[b, t // 64], t % 64, h, kv)
+        s, m = A.to_bf16(np.array([s, m], np.float32) * np.float32(f))
+        A.kv4_pack(self.cache, self.table[b, t // 64], t % 64, h, kv, codes, s, m)
+        vals, ss, ms = self.kv[b][kv]
+        vals[h, t], ss[h, t], ms[h, t] = A.kv4_values(codes, s, m), s, m
+
     def dev(self):
         self.d_cache = torch.from_numpy(self.cache).cuda()
         self.d_table = torch.from_numpy(self.table).cuda()
@@ -294,6 +324,48 @@ def attn_bound(q, kv, ref, scale, tile=False):
         dx = dx + abs(scale) * sq * np.max(np.abs(k), initial=0.0) * 2.0 ** -11
     vmax = np.max(np.abs(v), initial=0.0)
     return (2 * dx + 2.0 ** -12) * vmax + 2.0 ** -8 * 8 * np.max(vs, initial=0.0) + 2.0 ** -8 * np.abs(ref)
+
+
+def row_bound(q, kv, last, ref, scale, tile=False):
+    """Per row [n, D]: the bound by what the row sees."""
+    (k, ks, km), (v, vs, vm) = [tuple(np.asarray(x, np.float64) for x in side) for side in kv]
+    q = q.astype(np.float64)
+    D, tol = q.shape[-1], np.zeros(ref.shape)
+    for i in range(len(q)):
+        e = min(int(last[i]) + 1, len(k))
+        if e <= 0:
+            continue
+        x = k[:e] @ q[i] * scale
+        p = np.exp(x - x.max())
+        p /= p.sum()
+        va, sq = np.abs(v[:e]).max(-1), np.abs(q[i]).sum()
+        dx = abs(scale) * sq * 2.0 ** -23 * (143 * ks[:e] * (D // 8 + 4) + 3 * (np.abs(km[:e]) + 136 * ks[:e]))
+        dv = vs[:e] * (2.0 ** -8 + e / 16 * 23 * 2.0 ** -23)
+        if tile:
+            dx = dx + abs(scale) * sq * np.abs(k[:e]).max(-1) * 2.0 ** -10
+            dv = va * (2.0 ** -10 + 2.0 ** -11)
+        w = p * (np.exp(2 * np.minimum(dx, 300.0)) - 1 + 2.0 ** -20 + e * 2.0 ** -23)   # e^(2 dx) - 1 >= 2 dx
+        a = np.abs(ref[i])
+        tol[i] = (w * va).sum() + w.sum() * a + (p * dv).sum() + e * 2.0 ** -26 * (p * va).max() + 2.0 ** -8 * a
+    return tol
+
+
+def check_rows(bt, q, out, hq, scale, tile=False, heads=None, skip=0):
+    """Every row but a sequence's last `skip` within row_bound; returns the largest bound over the largest
+    magnitude of its row."""
+    o, g, worst = np_of(out).astype(np.float64), hq // bt.H, 0.0
+    for b, (c, n) in enumerate(zip(bt.ctx, bt.new)):
+        r = slice(bt.cu[b], bt.cu[b] + n - skip)
+        last = c - n + np.arange(n - skip)
+        for j in (heads or range(hq)):
+            kv = [tuple(a[j // g] for a in side) for side in bt.kv[b]]
+            ref = A.attend(q[r, j].astype(np.float64), kv[0][0], kv[1][0], last, scale)
+            tol = row_bound(q[r, j], kv, last, ref, scale, tile)
+            err = np.abs(o[r, j] - ref)
+            assert np.all(err <= tol), (b, j, np.argwhere(~(err <= tol))[0], err[~(err <= tol)][0], tol[~(err <= tol)][0])
+            seen = np.abs(ref).max(-1) > 0
+            worst = max(worst, (tol.max(-1)[seen] / np.abs(ref).max(-1)[seen]).max(initial=0.0))
+    return worst
 
 
 def check_attn(bt, q, out, hq, scale, sentinel=None, tile=False):
@@ -761,6 +833,73 @@ def test_long_context_keeps_bf16_accuracy(D):
         ref = A.attend(q[:, j].astype(np.float64), kv[0][0], kv[1][0], [19999], D ** -0.5)
         err = np.linalg.norm(np_of(out)[0, j] - ref[0]) / np.linalg.norm(ref[0])
         assert err <= 2.0 ** -7 / 12 ** 0.5 + 2.0 ** -12
+
+
+# ----------------------------------------------------------------------------- range
+FORMS = [(64, 0), (128, 0), (64, WIDE), (128, WIDE)]     # clusters or a run per row tile; runs and a join
+
+
+def call(bt, q, **kw):
+    return S.attn_kv4(torch.from_numpy(q).cuda().bfloat16(), bt.d_cache, bt.d_table, bt.d_lens, cu_q=bt.d_cu, **kw)
+
+
+@pytest.mark.parametrize("D,wide", FORMS)
+@pytest.mark.parametrize("ctx,new,same", [([1], [1], False), ([1, 70, 900], [1, 1, 1], False), ([9000], [1], True), ([2100, 130], [5, 3], True)])
+@pytest.mark.parametrize("value", [1.0, 256.0, 2.0 ** 22, 1e30, -3e38, 1e-30, 0.0])
+def test_constant_value_rows(value, ctx, new, same, D, wide):
+    """Value rows of one number (step 0): the output is that number, for one token, for thousands of equal
+    scores (keys of zero) and of unequal ones."""
+    bt = Batch(ctx, new, 2, D, seed=51, wide=wide).fill()
+    for b, c in enumerate(ctx):
+        for h in range(2):
+            for t in range(c):
+                bt.put(b, 1, h, t, np.full(D, value, np.float32))
+                if same:
+                    bt.put(b, 0, h, t, np.zeros(D, np.float32))
+    q = bf16_randn(bt.rng, (bt.T, 8, D))
+    out = call(bt.dev(), q, max_q=max(new))
+    assert S.device_error() == 0
+    check_rows(bt, q, out, 8, D ** -0.5, heads=[0, 5])
+    assert torch.all((out.double() / (value or 1.0) - (1.0 if value else 0.0)).abs() <= 2.0 ** -7)
+
+
+@pytest.mark.parametrize("D,wide", FORMS)
+@pytest.mark.parametrize("mag", [1e-33, 1e-20, 1e20, 1e36])
+def test_values_of_any_size(mag, D, wide):
+    bt = Batch([70, 500, 1000], [1, 5, 2], 2, D, seed=52, wide=wide).fill(vmag=mag)
+    q = bf16_randn(bt.rng, (bt.T, 8, D))
+    assert check_rows(bt, q, call(bt.dev(), q, max_q=5), 8, D ** -0.5) < 0.25 and S.device_error() == 0
+
+
+@pytest.mark.parametrize("D,wide", FORMS)
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("f", [2.0 ** 12, 2.0 ** 20, 1e30])
+def test_drafts_do_not_see_later_tokens(f, side, D, wide):
+    """The last draft's key or value made huge: the drafts before it stay within what they see."""
+    bt = Batch([300, 90], [5, 3], 2, D, seed=53, wide=wide).fill()
+    q = bf16_randn(bt.rng, (bt.T, 8, D))
+    for b, c in enumerate(bt.ctx):
+        for h in range(2):
+            bt.times(b, side, h, c - 1, f)
+    out = call(bt.dev(), q, max_q=5)
+    assert S.device_error() == 0
+    # (scores of 1e30 are beyond what fp32 can subtract: the rows that see such a key are left out)
+    check_rows(bt, q, out, 8, D ** -0.5, skip=1 if side == 0 and f > 2.0 ** 20 else 0)
+
+
+@pytest.mark.parametrize("D,wide", FORMS)
+@pytest.mark.parametrize("at", [0, 70, 699])
+@pytest.mark.parametrize("f", [2.0 ** 12, 2.0 ** 20, 2.0 ** 40, 1e30])
+def test_a_huge_value_without_weight_costs_nothing(f, at, D, wide):
+    """One token with huge values and a score far below the others', first, in the middle and last."""
+    bt = Batch([700], [3], 2, D, seed=54, wide=wide).fill()
+    q = bf16_randn(bt.rng, (3, 8, D))
+    q[..., 0] = 8.0
+    for h in range(2):
+        bt.times(0, 1, h, at, f)
+        bt.put(0, 0, h, at, np.concatenate([[-60.0 * D ** 0.5], np.zeros(D - 1)]).astype(np.float32))   # x about -480
+    out = call(bt.dev(), q, max_q=3)
+    assert check_rows(bt, q, out, 8, D ** -0.5) < 0.25 and S.device_error() == 0
 
 
 # ----------------------------------------------------------------------------- together

@@ -10,11 +10,15 @@
 // and l += sum p in fp32;  out = O / l.
 // Precision: decoded values are m + s c rounded once to fp16 (11 bits; bf16's 8 would cost the
 // scores of a peaked softmax several percent), after a division by a power of two that brings the
-// largest to about 2^-7: per page for keys (f takes it back), one running power for values (O is
-// rescaled when it has to grow).  There a code's bits are themselves an fp16, c 2^-24, and one FMA
-// makes the value.  Queries are bf16: a power of two per row makes them exact in fp16.
-// Probabilities are fp16 of values up to 2^15, the row's maximum at 2^10 or above: relative 2^-11
-// down to 2^-24 of the largest.
+// largest to about 2^-6: there a code's bits are themselves an fp16, c 2^-24, and one FMA makes the
+// value.  A page's keys and a step's values share a power where their tokens' sizes lie within 2^7 of
+// each other (fp16's subnormals then cost no more than its normal rounding); elsewhere every token has
+// its own.  The powers of keys multiply the scores, those of values the probabilities, before these are
+// rounded: P = fp16(2^(x - m) 2^(e + off)), e the value's power, m and off the row's own, so that no
+// row depends on the size of a token that it does not see or that has no weight in it.
+// Queries are bf16: a power of two per row makes them exact in fp16.
+// The largest P of a row is 2^9 to 2^16: relative 2^-11 down to 2^-23 of the largest.  References move by
+// whole powers of two: nothing that is stored is rounded by them (only what leaves fp16's range below).
 // Roles: warps 0-3 and 4-7 the softmax of a tile each (a thread owns a row: no shuffles), warps
 // 8-9 decode keys, 10-11 values, warp 12 issues the products, 13 copies pages (codes of keys and
 // values of a page are one bulk copy).  The tiles alternate: while one's softmax runs, the tensor
@@ -36,6 +40,7 @@
 //   P beside S (there is room for heads of 64), the next scores issued early: 3,900 to 4,200 for heads of 64
 //   a share of the exponentials as polynomials on the FMA pipe: 1 in 8 1% slower, 3 in 8 5% slower
 #include <algorithm>
+#include <cstddef>
 
 #include "attn.cuh"
 
@@ -48,8 +53,8 @@ constexpr int kKeys = 128;                 // tokens per step: two pages
 // Four warpgroups launched with 128 registers a thread (the last: issue, copies and two idle warps);
 // the softmax takes 176, the decoders 96, the last 64: 2 * 176 + 96 + 64 = 4 * 128.
 constexpr int kTileThreads = 16 * 32;
-constexpr int kInfoSlots = 4;
-constexpr float kUp = 10.0f;               // a probability of 1 is held as 2^10
+constexpr int kInfoSlots = 3;
+constexpr int kUp = 10;                    // the largest P of a row is 2^10 when its reference is set
 constexpr int kAllSeen = 0x7FFFFFFF - 2 * kKeys;
 constexpr int kTmemCols = 512;             // S0, S1 (128 columns each), O0, O1 (D each)
 constexpr long long kDrainLimit = 1000000000LL;
@@ -59,7 +64,7 @@ struct Tile {
     static constexpr int kQ = kRowsTile * D * 2;      // one tile's queries
     static constexpr int kOp = kKeys * D * 2;         // decoded keys or values of a step
     static constexpr int kPage = 2 * Kv4<D>::kBlock;  // a page of a head, as it is in the cache
-    static constexpr int kBars = 512;
+    static constexpr int kBars = 1024;
     // One CTA per SM in any case (its tensor memory), so heads of 64 ask for as much as keeps a second
     // one away.  No room is left for aligning the operands: the base is at 1024 (checked).
     static constexpr size_t kUse = 2 * kQ + 4 * kOp + 4 * kPage + kBars;
@@ -70,21 +75,27 @@ struct Tile {
 template <int N>
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRowsTile >> 4) << 24);
 
-// What the softmax has to know of a step.
-struct StepInfo {
-    float key_scale[2];   // a key of the first, second page is its fp16 value times this
+// What the softmax has to know of a step, with kOffset added to every power.
+constexpr int kOffset = 110;               // powers are -100 .. 134
+constexpr int kApart = 256;                // set in key_exp, value_exp: the tokens have powers of their own
+constexpr int kMostExp = 120;              // above it keys are taken token by token too (2^key_exp is a float below)
+constexpr int kBad = 255;                  // as a token's value power: the value is NaN
+struct alignas(16) StepInfo {
+    int key_exp[2];       // a key of the first, second page is its fp16 value times 2^key_exp
     int value_exp;        // a value is its fp16 value times 2^value_exp
     int there;            // bit 0, 1: the first, second page is in the cache
-    uint32_t bad[4];      // tokens 32 i + bit whose value is NaN
+    uint8_t key_of[kKeys], value_of[kKeys];  // the tokens' powers where they have their own
 };
 
+static_assert(offsetof(StepInfo, key_of) % 16 == 0 && offsetof(StepInfo, value_of) % 16 == 0, "read 16 bytes at a time");
+
 struct TileBars {
+    StepInfo info[kInfoSlots];
     uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], info_full[kInfoSlots];
     uint64_t s_full[2], p_full[2], o_full[2], raw_full[2], raw_empty[2], drain;
     uint32_t tmem;
     int abort;
     int there[2];            // of the raw pages
-    StepInfo info[kInfoSlots];
 };
 
 template <int N>
@@ -102,11 +113,10 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                    "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// Power of two to divide by so that magnitudes up to `most` become at most 2^(bits + 1).
-__device__ __forceinline__ int exp_for(float most, int bits) {
-    return max((int)(__float_as_uint(most) >> 23) - 127 - bits, -100);  // most >= 0 and finite
+// Power of two to divide by so that magnitudes up to `most` become at most 2^-6.
+__device__ __forceinline__ int exp_for(float most) {
+    return max((int)(__float_as_uint(most) >> 23) - 127 + 7, -100);  // most >= 0 and finite
 }
-
 // Two values m + s c, c the nibbles of x that MASK names, read as fp16 (c 2^-24, or c 2^-20 for the
 // nibbles one up): s is the step times 2^24 or 2^20 to match.
 template <uint32_t MASK>
@@ -126,9 +136,12 @@ __device__ __forceinline__ bool pair_bad(uint32_t sm) {
     return !(fabsf(kv4_low(sm)) < INFINITY && fabsf(kv4_low(sm) + 15.0f * kv4_step(sm)) < INFINITY);
 }
 
-// Maximum of non-negative floats over a warp.
-__device__ __forceinline__ float warp_max(float v) {
-    return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
+// The power that tokens of a warp's sizes `most` share, kOffset added, and kApart where they cannot: `least` is
+// the smallest size, any but 0 (those ask for no power: +inf), and 0 for a token that needs a look of its own.
+__device__ __forceinline__ int shared_exp(float least, float most) {
+    const int hi = (int)__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+    const int lo = (int)__reduce_min_sync(0xFFFFFFFFu, __float_as_uint(least));
+    return exp_for(__int_as_float(hi)) + kOffset + (lo < max((hi & 0x7F800000) - (7 << 23), 1) ? kApart : 0);
 }
 
 // One lane of a converged warp.
@@ -235,7 +248,18 @@ __device__ __forceinline__ bool find_tile(const AttnParams &p, int i, Place &w) 
     return false;
 }
 
-// 32 lanes x 32 bit, 16 consecutive columns: thread t writes lane (base + t).
+// 32 lanes x 32 bit, 8 or 16 consecutive columns: thread t reads or writes lane (base + t).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
@@ -244,62 +268,77 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-// A row's reference m of the exponentials and, in two halves, its sum of 2^(x - m + kUp).
+// A row's state: with x its scores, l = sum 2^(x - m) in two halves, and O is in units of 2^-off of that.
+// m and off are whole numbers.
 struct RowSums {
     float m;
+    int off;
     f2 l;
 };
 
-// Moves the reference of the rows that need it (the largest score of this part of the step is not
-// below it by kUp still, or nothing was seen before) and brings all that was computed against the
-// old one to the new one: the sum, the step's probabilities stored so far and, past the first step, O.
-// r: the part's scores, n: tokens of it that the row sees.
-template <int D>
-__device__ __forceinline__ void move_reference(uint32_t s_tmem, uint32_t o_tmem, int c0, uint32_t (&r)[32], float f, int n, bool first,
-                                               RowSums &row) {
-    float mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 32; i++) mx = fmaxf(mx, i < n ? __uint_as_float(r[i]) : -INFINITY);
-    mx = mx == -INFINITY ? mx : f * mx;  // 0 * -inf would be NaN
-    const float up = fmaxf(row.m, mx);
-    const float by = row.m == -INFINITY ? 0.0f : exp2_fast(row.m - up);
+// The factors that bring sums of 2^(x - m), and P and O, to a moved reference.
+struct Moved {
+    float l, o;
+};
+
+// Moves a row's reference: its largest score so far is at least mx (in the part at hand; -inf: none), and the
+// part's largest P is 2^(mp - m + off).  The part's largest becomes 2^kUp or what was there keeps its size,
+// whichever is lower.
+__device__ __forceinline__ Moved move_row(float mx, float mp, RowSums &row) {
+    const float up = fmaxf(row.m, ceilf(mx));
+    const bool fresh = row.m == -INFINITY;
+    if (up == -INFINITY) return {1.0f, 1.0f};
+    const float by = fresh ? -INFINITY : row.m - up;                                 // <= 0
+    const int keep = fresh ? 100000 : row.off + (int)fminf(-by, 1000.0f);
+    const int set = mp == -INFINITY ? 100000 : kUp + (int)floorf(fminf(up - mp, 1000.0f));
+    const int off = fresh && mp == -INFINITY ? row.off : min(keep, set);
+    const Moved f = {exp2_fast(by), exp2_fast(by + (float)(off - row.off))};
     row.m = up;
-    row.l = mul2(row.l, pair2(by, by));
+    row.off = off;
+    row.l = mul2(row.l, pair2(f.l, f.l));
+    return f;
+}
+
+// Brings the step's P of the parts before column c0 and, past the first step, O to moved references.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t s_tmem, uint32_t o_tmem, int c0, bool first, float by) {
     const uint32_t by2 = pack_f16(by, by);
 #pragma unroll 1
-    for (int c = 0; c < c0; c += 32) {  // probabilities of parts before this one
-        uint32_t q[16];
-        tmem_ld16(s_tmem + c / 2, q);
+    for (int c = 0; c < c0; c += 16) {
+        uint32_t q[8];
+        tmem_ld8(s_tmem + c / 2, q);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 16; k++) asm volatile("mul.rn.f16x2 %0, %0, %1;" : "+r"(q[k]) : "r"(by2));
-        tmem_st16(s_tmem + c / 2, q);
+        for (int k = 0; k < 8; k++) asm volatile("mul.rn.f16x2 %0, %0, %1;" : "+r"(q[k]) : "r"(by2));
+        tmem_st8(s_tmem + c / 2, q);
     }
     if (!first) {
         // the products up to the step before are complete: this step's S was issued after them
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-            tmem_ld32(o_tmem + c, r);
-            tmem_ld_wait32(r);
+        for (int c = 0; c < D; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(o_tmem + c, r);
+            tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; k++) r[k] = __float_as_uint(__uint_as_float(r[k]) * by);
-            tmem_st32(o_tmem + c, r);
+            for (int k = 0; k < 16; k++) r[k] = __float_as_uint(__uint_as_float(r[k]) * by);
+            tmem_st16(o_tmem + c, r);
         }
     }
     tmem_st_wait();
-    tmem_ld32(s_tmem + c0, r);  // this part's columns are not written yet
-    tmem_ld_wait32(r);
 }
 
-// P = 2^(f S - m + kUp) of the step as fp16 into the tensor memory of S (columns that are read already).
-// f0, f1 >= 0 scale the pages' scores.  MASK: the row sees the step's first `seen` tokens, of pages that
-// are there.  The reference lags behind the row's maximum: it moves only when 32 probabilities add up
-// to more than fp16 holds, or when a row sees its first token.
+// P = 2^(f S - m + e) of the step as fp16 into the tensor memory of S (columns that are read already), with
+// e = ve + off for all tokens.  f0, f1 >= 0 scale the pages' scores.  MASK: the row sees the step's first
+// `seen` tokens, of pages that are there.  References lag behind the rows' maxima: they move only when 32 P
+// add up to more than fp16 holds, or when a row sees its first token.
 template <int D, bool MASK>
-__device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, float f0, float f1, int seen, int there, bool first,
+__device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, float f0, float f1, int ve, int seen, int there, bool first,
                                            RowSums &row) {
     uint32_t buf[2][32];
     tmem_ld32(s_tmem, buf[0]);
+    // P is 2^(x + nm), and 2^(x - m) is P times un
+    float nm = row.m == -INFINITY ? 0.0f : (float)(ve + row.off) - row.m;
+    float un = __int_as_float((127 - min(ve + row.off, 126)) << 23);
 #pragma unroll 1
     for (int page = 0; page < 2; page++) {
         const float fp = page ? f1 : f0;
@@ -315,13 +354,11 @@ __device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, flo
             uint32_t pk[16];
             f2 sum;
             for (bool moved = false;; moved = true) {
-                const float ref = row.m == -INFINITY ? 0.0f : row.m - kUp;
-                const f2 nm = pair2(-ref, -ref);
                 f2 sum2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                     float a, b;
-                    split2(fma2(f, pair2u(r[i], r[i + 1]), nm), a, b);
+                    split2(fma2(f, pair2u(r[i], r[i + 1]), pair2(nm, nm)), a, b);
                     a = exp2_fast(a);
                     b = exp2_fast(b);
                     if (MASK) {
@@ -336,13 +373,67 @@ __device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, flo
                 split2(sum, a, b);
                 // once is enough (a row of nothing but NaN has no reference after it either)
                 if (moved || !__any_sync(0xFFFFFFFFu, a + b > 60000.0f || (row.m == -INFINITY && n > 0))) break;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 32; i++) mx = fmaxf(mx, i < n ? __uint_as_float(r[i]) : -INFINITY);
+                mx = mx == -INFINITY ? mx : fp * mx;  // 0 * -inf would be NaN
+                const Moved by = move_row(mx, mx + (float)ve, row);
                 tmem_ld_wait32(buf[half ^ 1]);
-                move_reference<D>(s_tmem, o_tmem, c0, r, fp, n, first, row);
+                rescale<D>(s_tmem, o_tmem, c0, first, by.o);
+                nm = row.m == -INFINITY ? 0.0f : (float)(ve + row.off) - row.m;
+                un = __int_as_float((127 - min(ve + row.off, 126)) << 23);
             }
-            row.l = add2(row.l, sum);
+            row.l = fma2(sum, pair2(un, un), row.l);
             tmem_st16(s_tmem + c0 / 2, pk);
         }
     }
+}
+
+// The same where tokens have powers of their own (key_of, value_of, with kOffset added; kBad: a value of NaN)
+// or the step's power is far from the row's: every probability for l, and its P apart.  Rare, so nothing overlaps,
+// and a call, out of the usual step's way in the instruction cache (inlined: prompts of 2,048 47.2 us against
+// 47.0, chunks 3.74 ms against 3.69).
+template <int D>
+__device__ __noinline__ RowSums step_apart(uint32_t s_tmem, uint32_t o_tmem, float row_scale, const StepInfo &info, int seen,
+                                           bool first, RowSums row) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < kKeys; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(s_tmem + c0, r);
+        const uint4 kb = *reinterpret_cast<const uint4 *>(info.key_of + c0), vb = *reinterpret_cast<const uint4 *>(info.value_of + c0);
+        const uint32_t kw[4] = {kb.x, kb.y, kb.z, kb.w}, vw[4] = {vb.x, vb.y, vb.z, vb.w};
+        tmem_ld_wait();
+        const int n = info.there >> (c0 / 64) & 1 ? seen - c0 : 0, page = info.key_exp[c0 / 64];
+        float x[16], e[16], mx = -INFINITY, mp = -INFINITY;
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const int ke = page & kApart ? kw[i / 4] >> (8 * (i & 3)) & 255 : page;
+            const int ve = info.value_exp & kApart ? vw[i / 4] >> (8 * (i & 3)) & 255 : info.value_exp;
+            // 2^(ke - kOffset) is a float up to 127: 2^7 of it goes to the row's factor
+            x[i] = i < n ? __uint_as_float(r[i]) * (row_scale * 128.0f) * __int_as_float((ke - kOffset - 7 + 127) << 23) : -INFINITY;
+            e[i] = (float)(ve - kOffset);
+            bad |= i < n && ve == kBad;
+            mx = fmaxf(mx, x[i]);
+            mp = fmaxf(mp, x[i] + e[i]);
+        }
+        const bool far = mx > row.m + 8.0f || mp - row.m + (float)row.off > 14.0f;
+        if (__any_sync(0xFFFFFFFFu, far)) {
+            const Moved by = far ? move_row(mx, mp, row) : Moved{1.0f, 1.0f};
+            rescale<D>(s_tmem, o_tmem, c0, first, by.o);
+        }
+        const float ref = row.m == -INFINITY ? 0.0f : row.m;
+        float sum = bad ? __int_as_float(0x7FFFFFFF) : 0.0f;
+        uint32_t pk[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            sum += exp2_fast(x[i] - ref) + exp2_fast(x[i + 1] - ref);
+            pk[i / 2] = pack_f16(exp2_fast(x[i] - ref + (e[i] + (float)row.off)), exp2_fast(x[i + 1] - ref + (e[i + 1] + (float)row.off)));
+        }
+        row.l = add2(row.l, pair2(sum, 0.0f));
+        tmem_st8(s_tmem + c0 / 2, pk);
+    }
+    return row;
 }
 
 template <int D>
@@ -351,7 +442,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *sq = smem, *sk = sq + 2 * T::kQ, *sv = sk + 2 * T::kOp, *raw = sv + 2 * T::kOp;
     TileBars *bar = reinterpret_cast<TileBars *>(raw + 4 * T::kPage);
-    static_assert(sizeof(TileBars) <= T::kBars, "barriers");
+    static_assert(sizeof(TileBars) <= T::kBars && T::kPage % 16 == 0, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -362,7 +453,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     const int hi_row = min(row0 + kRowsCta, nrow) - 1;
     // steps: up to the last token that the last row sees, and no further than the table
     const int keys = min(pos0 + hi_row / p.g + 1, p.c.width * SHERRY_KV4_PAGE);
-    const int steps = keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
+    const int steps = keys > 0 ? (keys - 1) / kKeys + 1 : 0;
     const long long limit = p.wait_limit;
     if (smem_u32(smem) & 1023) {  // the swizzled operands need it
         if (threadIdx.x == 0) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_UNSUPPORTED);
@@ -423,7 +514,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                 for (int k = 0; k < 4; k++)
                     most = fmaxf(most, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
             }
-            const int qe = exp_for(fminf(most, 3e38f), 7);
+            const int qe = max((int)(__float_as_uint(fminf(most, 3e38f)) >> 23) - 127 - 7, -100);  // the largest below 2^8
             const float down = copysignf(pow2(-qe), p.scale2);  // scores come out with the scale's sign
             row_scale = fabsf(p.scale2) * pow2(qe);
 #pragma unroll 4
@@ -446,49 +537,30 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_base + i * kKeys;
         const uint32_t o_tmem = tmem + lane_base + 2 * kKeys + i * D;
-        RowSums row = {-INFINITY, pair2(0.0f, 0.0f)};
-        int oe = 0;                     // O is in units of 2^oe
+        RowSums row = {-INFINITY, 0, pair2(0.0f, 0.0f)};
         bool dead = false;
+        int slot = 0;
+        uint32_t lap = 0;
         for (int j = 0; j < steps; j++) {
-            const int slot = j % kInfoSlots;
-            if (!warp_wait(&bar->info_full[slot], (j / kInfoSlots) & 1, abort, p.err, limit) ||
+            if (!warp_wait(&bar->info_full[slot], lap, abort, p.err, limit) ||
                 !warp_wait(&bar->s_full[i], j & 1, abort, p.err, limit)) {
                 dead = true;
                 break;
             }
             tc_fence_after();
             const StepInfo &info = bar->info[slot];
+            if (++slot == kInfoSlots) slot = 0, lap ^= 1;
             const int there = info.there, t0 = j * kKeys;
-            const float f0 = row_scale * info.key_scale[0], f1 = row_scale * info.key_scale[1];
             const int seen = min(max(last - t0 + 1, 0), kKeys);
-            const bool whole = there == 3 && t0 + kKeys - 1 <= last_min;
-            const int ve = info.value_exp;
-            if (ve != oe) {
-                if (j > 0) {
-                    const float f = pow2(oe - ve);
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_tmem + c0, o);
-                        tmem_ld_wait32(o);
-#pragma unroll
-                        for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        tmem_st32(o_tmem + c0, o);
-                    }
-                    tmem_st_wait();
-                }
-                oe = ve;
-            }
-            if (whole) step_probs<D, false>(s_tmem, o_tmem, f0, f1, seen, there, j == 0, row);
-            else step_probs<D, true>(s_tmem, o_tmem, f0, f1, seen, there, j == 0, row);
-            if ((info.bad[0] | info.bad[1] | info.bad[2] | info.bad[3]) != 0) {
-                // a value of NaN is zero in the operand: the rows that see it get their NaN here
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const int n = seen - 32 * k;
-                    const uint32_t mine = n >= 32 ? 0xFFFFFFFFu : n > 0 ? (1u << n) - 1u : 0u;
-                    if (info.bad[k] & mine) row.l = pair2(__int_as_float(0x7FFFFFFF), 0.0f);
-                }
+            const int k0 = info.key_exp[0], k1 = info.key_exp[1], v = info.value_exp, ve = v - kOffset;
+            // a row whose P would all be far below or above its largest takes the step token by token too
+            const bool far = row.m != -INFINITY && (ve + row.off < -40 || ve + row.off > 100);
+            if (__any_sync(0xFFFFFFFFu, far || (k0 | k1 | v) & kApart)) {
+                row = step_apart<D>(s_tmem, o_tmem, row_scale, info, seen, j == 0, row);
+            } else {
+                const float f0 = row_scale * __int_as_float((k0 - kOffset + 127) << 23), f1 = row_scale * __int_as_float((k1 - kOffset + 127) << 23);
+                if (there == 3 && t0 + kKeys - 1 <= last_min) step_probs<D, false>(s_tmem, o_tmem, f0, f1, ve, seen, there, j == 0, row);
+                else step_probs<D, true>(s_tmem, o_tmem, f0, f1, ve, seen, there, j == 0, row);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -501,7 +573,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             float l, l1;
             split2(row.l, l, l1);
             l += l1;
-            const float inv = l == 0.0f ? 0.0f : pow2(oe - (int)kUp) / (l * pow2(-(int)kUp));
+            // out = O 2^-off / l, the power in two halves (values near the ends of fp32's range)
+            const float half = pow2(-row.off >> 1), inv = l == 0.0f ? 0.0f : pow2(-row.off - (-row.off >> 1)) / l;
             uint16_t *dst = p.out + (long long)(w.first + rw / p.g) * p.out_stride + (long long)(h * p.g + rw % p.g) * D;
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -519,7 +592,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                         uint32_t u[4];
 #pragma unroll
                         for (int e = 0; e < 4; e++)
-                            u[e] = pack_bf16(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
+                            u[e] = pack_bf16(__uint_as_float(o[k + 2 * e]) * half * inv, __uint_as_float(o[k + 2 * e + 1]) * half * inv);
                         *reinterpret_cast<uint4 *>(dst + c0 + k) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
@@ -530,27 +603,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         if (warp < 10) {
         // ---------------- keys: a warp per page, two tokens per thread ----------------
         const int k = warp - 8;
-        for (int j = 0; j < steps; j++) {
-            const int slot = j % kInfoSlots, s = j & 1;
+        for (int j = 0, slot = 0; j < steps; j++) {
+            const int s = j & 1;
             if (!warp_wait(&bar->raw_full[s], (j >> 1) & 1, abort, p.err, limit)) break;
             const uint8_t *blk = raw + (2 * s + k) * T::kPage;
             const int there = bar->there[s];
-            // tokens past the sequence's end may hold anything: they count as zeros
-            const int in = there >> k & 1 ? w.len - j * kKeys - k * SHERRY_KV4_PAGE : 0;
+            // tokens past the last that a row of this CTA sees may hold anything: they count as zeros
+            const int in = there >> k & 1 ? keys - j * kKeys - k * SHERRY_KV4_PAGE : 0;
             const uint32_t *pairs = reinterpret_cast<const uint32_t *>(blk + Kv4<D>::kCodes);
             const uint32_t sm[2] = {lane < in ? pairs[lane] : 0u, lane + 32 < in ? pairs[lane + 32] : 0u};
-            const int e = exp_for(warp_max(fmaxf(pair_most(sm[0]), pair_most(sm[1]))), -7);
-            // The slot is free: k_empty of step j - 3 was waited for, and its products were issued after
-            // the softmax of step j - 4 was done.
+            const float size[2] = {pair_most(sm[0]), pair_most(sm[1])};
+            auto some = [](float v) { return v == 0.0f ? INFINITY : v; };
+            int shared = shared_exp(fminf(some(size[0]), some(size[1])), fmaxf(size[0], size[1]));
+            if (shared > kOffset + kMostExp) shared |= kApart;
+            const int e = (shared & (kApart - 1)) - kOffset;
+            int own[2] = {e, e};
+            if (!warp_wait(&bar->k_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
+            // The slot is free: the products of step j - 2 are complete, and their last half was issued after the
+            // softmax of step j - 3.
+            StepInfo &info = bar->info[slot];
             if (lane == 0) {
-                bar->info[slot].key_scale[k] = pow2(e);
-                if (k == 0) bar->info[slot].there = there;
+                info.key_exp[k] = shared;
+                if (k == 0) info.there = there;
+            }
+            if (shared & kApart) {
+                own[0] = exp_for(size[0]), own[1] = exp_for(size[1]);
+                info.key_of[SHERRY_KV4_PAGE * k + lane] = (uint8_t)(own[0] + kOffset);
+                info.key_of[SHERRY_KV4_PAGE * k + lane + 32] = (uint8_t)(own[1] + kOffset);
             }
             warp_arrive(&bar->info_full[slot]);
-            if (!warp_wait(&bar->k_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
-            const float down = pow2(-e);
+            if (++slot == kInfoSlots) slot = 0;
 #pragma unroll 1
             for (int t = 0; t < 2; t++) {
+                const float down = pow2(-own[t]);
                 const int row = lane + 32 * t, tok = SHERRY_KV4_PAGE * k + row;
                 const float st = kv4_step(sm[t]) * down, lo = kv4_low(sm[t]) * down;
                 const uint32_t s0 = pack_f16(st * 16777216.0f, st * 16777216.0f), s1 = pack_f16(st * 1048576.0f, st * 1048576.0f);
@@ -584,43 +669,57 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
         const int k = warp - 10;
         const int grp = lane & 7, qd = lane >> 3;  // tokens 8 grp ... of the page, word qd of each four
         const int odd = grp & 1;                   // these read the tokens of a pair in the other order, for the banks
-        int ve = -1000;                            // both warps follow the same values' power of two
-        for (int j = 0; j < steps; j++) {
-            const int slot = j % kInfoSlots, s = j & 1;
+        for (int j = 0, slot = 0; j < steps; j++) {
+            const int s = j & 1;
             if (!warp_wait(&bar->raw_full[s], (j >> 1) & 1, abort, p.err, limit)) break;
             const int there = bar->there[s];
             const uint8_t *blk = raw + 2 * s * T::kPage + Kv4<D>::kBlock;  // the first page's values
-            uint32_t all[4];                       // pairs of tokens lane + 32 i of the step
+            uint32_t pair[4];                                              // of tokens lane + 32 i of the step
+            float least = INFINITY, most = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const bool in = (there >> (i / 2) & 1) && j * kKeys + lane + 32 * i < w.len;
-                all[i] = in ? reinterpret_cast<const uint32_t *>(blk + (i / 2) * T::kPage + Kv4<D>::kCodes)[lane + 32 * (i & 1)] : 0u;
+                const bool in = (there >> (i / 2) & 1) && j * kKeys + lane + 32 * i < keys;
+                pair[i] = in ? reinterpret_cast<const uint32_t *>(blk + (i / 2) * T::kPage + Kv4<D>::kCodes)[lane + 32 * (i & 1)] : 0u;
+                const float size = pair_most(pair[i]);
+                least = fminf(least, size != 0.0f ? size : pair_bad(pair[i]) ? 0.0f : INFINITY);
+                most = fmaxf(most, size);
             }
-            const float most = warp_max(fmaxf(fmaxf(pair_most(all[0]), pair_most(all[1])), fmaxf(pair_most(all[2]), pair_most(all[3]))));
-            // 2^-8 when it is set; it follows when values reach 2^-6
-            if (exp_for(most, -7) > ve) ve = exp_for(most, -8);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t bad = __ballot_sync(0xFFFFFFFFu, pair_bad(all[i]));
-                if (k == 0 && lane == 0) bar->info[slot].bad[i] = bad;
-            }
-            if (k == 0 && lane == 0) bar->info[slot].value_exp = ve;
-            // free as the keys' part is: v_empty of step j - 3 was waited for
-            warp_arrive(&bar->info_full[slot]);
+            const int shared = shared_exp(least, most);
+            const int ve = (shared & (kApart - 1)) - kOffset;
+            const bool apart = shared & kApart;
             blk += k * T::kPage;
-            const int in = there >> k & 1 ? w.len - j * kKeys - k * SHERRY_KV4_PAGE - 8 * grp : 0;  // tokens of the eight that are there
-            const float down = pow2(-ve);
+            const int in = there >> k & 1 ? keys - j * kKeys - k * SHERRY_KV4_PAGE - 8 * grp : 0;  // tokens of the eight that are there
             uint32_t s0[4], s1[4], m2[4];
+            const float down = pow2(-ve);
 #pragma unroll
             for (int t = 0; t < 4; t++) {
                 const uint2 u = *reinterpret_cast<const uint2 *>(blk + Kv4<D>::kCodes + 4 * (8 * grp + 2 * t));
-                const uint32_t a = 2 * t < in && !pair_bad(u.x) ? u.x : 0u, b = 2 * t + 1 < in && !pair_bad(u.y) ? u.y : 0u;
-                const float sa = kv4_step(a) * down, sb = kv4_step(b) * down;
+                uint32_t a = 2 * t < in ? u.x : 0u, b = 2 * t + 1 < in ? u.y : 0u;
+                float da = down, db = down;
+                if (apart) {
+                    if (pair_bad(a)) a = 0u;
+                    if (pair_bad(b)) b = 0u;
+                    da = pow2(-exp_for(pair_most(a)));
+                    db = pow2(-exp_for(pair_most(b)));
+                }
+                const float sa = kv4_step(a) * da, sb = kv4_step(b) * db;
                 s0[t] = pack_f16(sa * 16777216.0f, sb * 16777216.0f);
                 s1[t] = pack_f16(sa * 1048576.0f, sb * 1048576.0f);
-                m2[t] = pack_f16(kv4_low(a) * down, kv4_low(b) * down);
+                m2[t] = pack_f16(kv4_low(a) * da, kv4_low(b) * db);
             }
             if (!warp_wait(&bar->v_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
+            // The slot is free: the products of step j - 2 are complete, and they were issued after its softmax.
+            StepInfo &info = bar->info[slot];
+            if (k == 0) {
+                if (lane == 0) info.value_exp = shared;
+                if (apart) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        info.value_of[lane + 32 * i] = (uint8_t)(pair_bad(pair[i]) ? kBad : kOffset + exp_for(pair_most(pair[i])));
+                }
+            }
+            warp_arrive(&bar->info_full[slot]);
+            if (++slot == kInfoSlots) slot = 0;
             const uint32_t sel_lo = odd ? 0x1054u : 0x5410u, sel_hi = odd ? 0x3276u : 0x7632u;
             uint8_t *dst = sv + s * T::kOp + k * (D * 128);
             const uint8_t *src = blk + 8 * grp * Kv4<D>::kRow;

@@ -902,6 +902,125 @@ def test_a_huge_value_without_weight_costs_nothing(f, at, D, wide):
     assert check_rows(bt, q, out, 8, D ** -0.5) < 0.25 and S.device_error() == 0
 
 
+TILE_HEADS = [0, 13, 31]
+
+
+def tile_batch(D, seed, ctx=(433,), new=(330,), **fill):
+    bt = Batch(list(ctx), list(new), 8, D, seed).fill(**fill)
+    assert is_tiles(bt, 32)
+    return bt
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("side", [0, 1])
+@pytest.mark.parametrize("at", [300, 383, 412])
+@pytest.mark.parametrize("f", [2.0 ** 12, 2.0 ** 20, 1e30])
+def test_tiles_rows_do_not_see_later_tokens(f, at, side, D):
+    """One token's key or value made huge: the rows before it stay within what they see, and the rows after
+    a value of that size too."""
+    bt = tile_batch(D, 61)
+    q = bf16_randn(bt.rng, (bt.T, 32, D))
+    for h in range(8):
+        bt.times(0, side, h, at, f)
+    out = call(bt.dev(), q)
+    assert S.device_error() == 0
+    # (scores of 1e30 are beyond what fp32 can subtract: the rows that see such a key are left out)
+    check_rows(bt, q, out, 32, D ** -0.5, tile=True, heads=TILE_HEADS, skip=433 - at if side == 0 and f > 2.0 ** 20 else 0)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [0, 70, 290])
+@pytest.mark.parametrize("f", [2.0 ** 12, 2.0 ** 20, 2.0 ** 40, 1e30])
+def test_tiles_a_huge_value_without_weight_costs_nothing(f, at, D):
+    bt = tile_batch(D, 62)
+    q = bf16_randn(bt.rng, (bt.T, 32, D))
+    q[..., 0] = 8.0
+    for h in range(8):
+        bt.times(0, 1, h, at, f)
+        bt.put(0, 0, h, at, np.concatenate([[-60.0 * D ** 0.5], np.zeros(D - 1)]).astype(np.float32))   # x about -480
+    out = call(bt.dev(), q)
+    assert S.device_error() == 0
+    check_rows(bt, q, out, 32, D ** -0.5, tile=True, heads=TILE_HEADS)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("mag", [1e-33, 1e-20, 1e20, 1e36])
+def test_tiles_values_of_any_size(mag, D):
+    bt = tile_batch(D, 63, ctx=(433, 3), new=(330, 9), vmag=mag)
+    q = bf16_randn(bt.rng, (bt.T, 32, D))
+    check_rows(bt, q, call(bt.dev(), q), 32, D ** -0.5, tile=True, heads=TILE_HEADS)
+    assert S.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("power", [-90, -13, 60, 110])
+def test_a_power_of_two_of_the_values_comes_out_exactly(power, tile, D):
+    """Every rounding commutes with powers of two, as long as nothing leaves fp32's normal range."""
+    bt = tile_batch(D, 67) if tile else Batch([433, 70], [3, 1], 8, D, 67).fill()
+    q = bf16_randn(bt.rng, (bt.T, 32, D))
+    ref = call(bt.dev(), q, max_q=max(bt.new))
+    for b, c in enumerate(bt.ctx):
+        for h in range(8):
+            for t in range(c):
+                bt.times(b, 1, h, t, 2.0 ** power)
+    assert torch.equal(call(bt.dev(), q, max_q=max(bt.new)).double() * 2.0 ** -power, ref.double())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("value", [1.0, 2.0 ** 22, 1e30, -3e38, 1e-30, 0.0])
+def test_tiles_constant_value_rows(value, D):
+    bt = tile_batch(D, 64)
+    for h in range(8):
+        for t in range(433):
+            bt.put(0, 1, h, t, np.full(D, value, np.float32))
+    q = bf16_randn(bt.rng, (bt.T, 32, D))
+    out = call(bt.dev(), q)
+    assert S.device_error() == 0
+    assert torch.all((out.double() / (value or 1.0) - (1.0 if value else 0.0)).abs() <= 2.0 ** -7)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["pages up", "pages down", "steps up", "steps down", "tokens", "tokens and keys", "one small"])
+def test_tiles_tokens_of_very_different_size(kind, D):
+    """Values (and keys) whose size changes a hundredfold or more from page to page or token to token."""
+    bt = tile_batch(D, 65, ctx=(640, 433), new=(330, 300))
+    for b, c in enumerate(bt.ctx):
+        for h in range(8):
+            for t in range(c):
+                if kind.startswith("pages"):
+                    bt.times(b, 1, h, t, 10.0 ** (t // 64 if kind == "pages up" else -(t // 64)))
+                elif kind.startswith("steps"):   # all alike within a step of 128 tokens, 1e9 from one to the next
+                    bt.times(b, 1, h, t, 1e9 ** ((t // 128 if kind == "steps up" else -(t // 128)) + 0.5 * (b - 1)))
+                elif kind == "one small":
+                    if t % 64 == 5:
+                        bt.times(b, 1, h, t, 1e-4), bt.times(b, 0, h, t, 1e-4)
+                else:
+                    bt.times(b, 1, h, t, 10.0 ** bt.rng.uniform(-9, 9))
+                    if kind == "tokens and keys":
+                        bt.times(b, 0, h, t, 10.0 ** bt.rng.uniform(-6, 0.5))
+    q = bf16_randn(bt.rng, (bt.T, 32, D))
+    out = call(bt.dev(), q)
+    assert S.device_error() == 0
+    check_rows(bt, q, out, 32, D ** -0.5, tile=True, heads=TILE_HEADS)
+
+
+@pytest.mark.parametrize("kv", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiles_nan_beside_tokens_of_very_different_size(kv, D):
+    bt = tile_batch(D, 66)
+    for h in range(8):
+        for t in range(433):
+            bt.times(0, 1, h, t, 10.0 ** bt.rng.uniform(-9, 9))
+    bt.cache[bt.table[0, 300 // 64], 3, kv, 32 * D + 4 * (300 % 64):32 * D + 4 * (300 % 64) + 4] = 0xFF   # token 300, head 3
+    q = bf16_randn(bt.rng, (bt.T, 32, D))
+    out = call(bt.dev(), q)
+    bad = torch.isnan(out).any(-1)      # row i is position 103 + i
+    assert bad[197:, 12:16].all() and not bad[:197].any() and not bad[:, :12].any() and not bad[:, 16:].any()
+    check_rows(bt, q, out, 32, D ** -0.5, tile=True, heads=[0, 31])
+    check_rows(bt, q, out, 32, D ** -0.5, tile=True, heads=[13], skip=330 - 197)
+
+
 # ----------------------------------------------------------------------------- together
 @pytest.mark.parametrize("D,hq,H", [(64, 8, 2), (128, 4, 2)])
 def test_attention_block_between_gemvs(D, hq, H):

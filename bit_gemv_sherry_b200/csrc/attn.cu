@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
             most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-            const int e = max((int)(__float_as_uint(most) >> 23) - 127 - 13, -100);  // the largest below 2^14
+            const int e = max((int)(__float_as_uint(most) >> 23) - 127 - 13, -120);  // the largest below 2^14
             const float d0 = pow2(-e), d1 = d0 * 0.0625f;
 #pragma unroll
             for (int w = 0; w < WK; w++) {

@@ -76,7 +76,7 @@ template <int N>
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRowsTile >> 4) << 24);
 
 // What the softmax has to know of a step, with kOffset added to every power.
-constexpr int kOffset = 110;               // powers are -100 .. 134
+constexpr int kOffset = 120;               // powers are -119 .. 134
 constexpr int kApart = 256;                // set in key_exp, value_exp: the tokens have powers of their own
 constexpr int kMostExp = 120;              // above it keys are taken token by token too (2^key_exp is a float below)
 constexpr int kBad = 255;                  // as a token's value power: the value is NaN
@@ -115,7 +115,7 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
 
 // Power of two to divide by so that magnitudes up to `most` become at most 2^-6.
 __device__ __forceinline__ int exp_for(float most) {
-    return max((int)(__float_as_uint(most) >> 23) - 127 + 7, -100);  // most >= 0 and finite
+    return max((int)(__float_as_uint(most) >> 23) - 127 + 7, -119);  // most >= 0 and finite
 }
 // Two values m + s c, c the nibbles of x that MASK names, read as fp16 (c 2^-24, or c 2^-20 for the
 // nibbles one up): s is the step times 2^24 or 2^20 to match.
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                 for (int k = 0; k < 4; k++)
                     most = fmaxf(most, fmaxf(fabsf(__uint_as_float(e[k] << 16)), fabsf(__uint_as_float(e[k] & 0xFFFF0000u))));
             }
-            const int qe = max((int)(__float_as_uint(fminf(most, 3e38f)) >> 23) - 127 - 7, -100);  // the largest below 2^8
+            const int qe = max((int)(__float_as_uint(fminf(most, 3e38f)) >> 23) - 127 - 7, -120);  // the largest below 2^8
             const float down = copysignf(pow2(-qe), p.scale2);  // scores come out with the scale's sign
             row_scale = fabsf(p.scale2) * pow2(qe);
 #pragma unroll 4

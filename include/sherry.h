@@ -562,8 +562,8 @@ sherry_status sherry_kv4_read(const sherry_kv4 *c, void *k, void *v, int type, i
  * head h, with the cache's head h / (Hq / H):
  *     out = sum_t p[t] v[t],  p = softmax over t = 0 .. pos of scale * (q . k[t]),
  * with k and v the values the cache holds.  A row without a position (pos < 0) gives zeros.
- * Sums and softmax statistics are fp32, the result is rounded once to bf16 (scores beyond 2^30, or sums
- * of values beyond fp32, are not served).  Few new tokens: the first product runs on the codes, exactly,
+ * Sums and softmax statistics are fp32, the result is rounded once to bf16 (queries beyond
+ * 2^112, scores beyond 2^30 and sums of values beyond fp32 are not served).  Few new tokens: the first product runs on the codes, exactly,
  * and a probability times its token's step is rounded to fp16 for the second: 2^-11 relative, down to
  * 2^-21 of the row's largest such product, 2^-32 of that below.  Many (prompts): keys, values and
  * probabilities are rounded to fp16 after powers of two that bring them into its range, 2^-10

@@ -871,6 +871,30 @@ def test_values_of_any_size(mag, D, wide):
     assert check_rows(bt, q, call(bt.dev(), q, max_q=5), 8, D ** -0.5) < 0.25 and S.device_error() == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("power", [-118, -60, 60, 105])
+def test_queries_and_keys_of_any_size(power, tile, D):
+    """Queries times a power of two and keys divided by it: the same scores, to the bit where no power of the
+    kernels' own stops short of them (keys of 2^118 are taken token by token, each with its own rounding)."""
+    bt = Batch([433], [330], 8, D, 68) if tile else Batch([433, 70], [3, 1], 8, D, 68)
+    bt.fill()
+    assert is_tiles(bt, 32) or not tile
+    q = bf16_randn(bt.rng, (bt.T, 32, D))
+    q = np.where(np.abs(q) < 2.0 ** -7, np.float32(0), q)      # (no query below the normal numbers)
+    ref = call(bt.dev(), q, max_q=max(bt.new))
+    check_rows(bt, q, ref, 32, D ** -0.5, tile=tile, heads=[0])
+    for b, c in enumerate(bt.ctx):
+        for h in range(8):
+            for t in range(c):
+                bt.times(b, 0, h, t, 2.0 ** -power)
+    q *= np.float32(2.0 ** power)
+    out = call(bt.dev(), q, max_q=max(bt.new))
+    check_rows(bt, q, out, 32, D ** -0.5, tile=tile, heads=[0, 31])
+    assert abs(power) > 110 or torch.equal(out, ref)
+    assert S.device_error() == 0
+
+
 @pytest.mark.parametrize("D,wide", FORMS)
 @pytest.mark.parametrize("side", [0, 1])
 @pytest.mark.parametrize("f", [2.0 ** 12, 2.0 ** 20, 1e30])
@@ -944,7 +968,7 @@ def test_tiles_a_huge_value_without_weight_costs_nothing(f, at, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("mag", [1e-33, 1e-20, 1e20, 1e36])
+@pytest.mark.parametrize("mag", [1e-34, 1e-20, 1e20, 1e36])
 def test_tiles_values_of_any_size(mag, D):
     bt = tile_batch(D, 63, ctx=(433, 3), new=(330, 9), vmag=mag)
     q = bf16_randn(bt.rng, (bt.T, 32, D))

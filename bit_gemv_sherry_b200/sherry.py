@@ -704,6 +704,15 @@ def _vector(t, name, dev, n=None):
         raise ValueError("%s must be contiguous with %s elements" % (name, n))
 
 
+def _bytes(t, name, dev):
+    """Size of a scratch buffer given by the caller, which kernels write to."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8 or t.get_device() != dev:
+        raise TypeError("%s must be a uint8 tensor on CUDA device %d" % (name, dev))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.numel()
+
+
 def _call(dev, f, where, *args):
     """f(*args, current stream of device dev), with dev the current device."""
     if _get_device() != dev:
@@ -860,7 +869,8 @@ def attn_kv4(q, cache, page_table, ctx_lens, cu_q=None, max_q=0, scale=None, out
     """Causal attention of the new tokens' q bf16 [T, Hq, dim] over the cache (their own keys and values
     written before): out bf16 [T, Hq, dim].  page_table, ctx_lens and cu_q as for kv4_write; scale
     defaults to dim ** -0.5; max_q, the most new tokens of a sequence, helps to pick kernels (0: not
-    known).  Rows without a position give zeros."""
+    known); ws, scratch of attn_kv4_workspace_bytes(T, Hq, dim) bytes on the same device.  Rows without a
+    position give zeros."""
     dev = _device(cache, "cache")
     ty, T, Hq, D, qs = _heads(q, "q", dev)
     args, H, cD = _kv4(cache, page_table, ctx_lens, cu_q, T, dev)
@@ -880,8 +890,11 @@ def attn_kv4(q, cache, page_table, ctx_lens, cu_q=None, max_q=0, scale=None, out
             ws = _workspaces.get((dev, _raw_stream(dev)))
         if ws is None or ws.numel() < need:
             ws = _scratch(need, dev)
+        nbytes = ws.numel()
+    else:
+        nbytes = _bytes(ws, "ws", dev)
     _call(dev, lib().sherry_attn_kv4, "sherry_attn_kv4", args, q.data_ptr(), qs, out.data_ptr(), os_, Hq, int(max_q),
-          D ** -0.5 if scale is None else scale, ws.data_ptr(), ws.numel())
+          D ** -0.5 if scale is None else scale, ws.data_ptr(), nbytes)
     return out
 
 

@@ -115,3 +115,10 @@ def test_binding_refuses_cpu_tensors():
         S.attn_kv4(q.bfloat16(), cache, i.view(1, 1), i)
     with pytest.raises(ValueError):
         S.kv4_cache(1, 2, 96, "cpu")
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(64, dtype=torch.uint8), torch.zeros(64), None, 4096])
+def test_binding_refuses_scratch_of_another_device_or_type(ws):
+    """What attn_kv4 asks of the caller's scratch before a kernel gets its address."""
+    with pytest.raises(TypeError):
+        S._bytes(ws, "ws", 0)

@@ -1104,3 +1104,20 @@ def test_c_entry_with_a_strided_table_and_workspace_of_the_stated_size():
     torch.cuda.synchronize()
     assert torch.equal(o, out) and torch.all(ws[need:] == 0xA5)
     assert torch.equal(S.attn_kv4(dq, bt.d_cache, wide[:, :bt.width], bt.d_lens), out)
+
+
+def test_attn_refuses_scratch_of_another_device_or_type():
+    bt = Batch([70], [1], 2, 64, seed=22).fill().dev()
+    q = torch.zeros(1, 4, 64, dtype=BF, device="cuda")
+    need = S.attn_kv4_workspace_bytes(1, 4, 64)
+    args = (q, bt.d_cache, bt.d_table, bt.d_lens)
+    for ws in (torch.zeros(need, dtype=torch.uint8), torch.zeros(need, dtype=torch.int8, device="cuda"),
+               torch.zeros(need, device="cuda")):
+        with pytest.raises(TypeError):
+            S.attn_kv4(*args, ws=ws)
+    with pytest.raises(ValueError):
+        S.attn_kv4(*args, ws=torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2])
+    with pytest.raises(RuntimeError):
+        S.attn_kv4(*args, ws=torch.zeros(need - 1, dtype=torch.uint8, device="cuda"))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(S.attn_kv4(*args, ws=ws), S.attn_kv4(*args)) and S.device_error() == 0

@@ -390,48 +390,63 @@ __device__ __forceinline__ void step_probs(uint32_t s_tmem, uint32_t o_tmem, flo
 }
 
 // The same where tokens have powers of their own (key_of, value_of, with kOffset added; kBad: a value of NaN)
-// or the step's power is far from the row's: every probability for l, and its P apart.  Rare, so nothing overlaps,
-// and a call, out of the usual step's way in the instruction cache (inlined: prompts of 2,048 47.2 us against
-// 47.0, chunks 3.74 ms against 3.69).
+// or the step's power is far from the row's: one exponential of every score for l, another with its value's power
+// for P.  Rare, so a call, out of the usual step's way in the instruction cache (inlined: prompts of 2,048 47.2 us
+// against 47.0, chunks of 4,096 at 16,384 3.74 ms against 3.69).  A prompt of 2,048 with one such step for each
+// 256 rows takes 55 us, with all of them 96.
 template <int D>
 __device__ __noinline__ RowSums step_apart(uint32_t s_tmem, uint32_t o_tmem, float row_scale, const StepInfo &info, int seen,
                                            bool first, RowSums row) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll 1
-    for (int c0 = 0; c0 < kKeys; c0 += 16) {
-        uint32_t r[16];
-        tmem_ld16(s_tmem + c0, r);
-        const uint4 kb = *reinterpret_cast<const uint4 *>(info.key_of + c0), vb = *reinterpret_cast<const uint4 *>(info.value_of + c0);
-        const uint32_t kw[4] = {kb.x, kb.y, kb.z, kb.w}, vw[4] = {vb.x, vb.y, vb.z, vb.w};
-        tmem_ld_wait();
-        const int n = info.there >> (c0 / 64) & 1 ? seen - c0 : 0, page = info.key_exp[c0 / 64];
-        float x[16], e[16], mx = -INFINITY, mp = -INFINITY;
-        bool bad = false;
+    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+        uint32_t r[32];
+        float e[32];
+        tmem_ld32(s_tmem + c0, r);
+        const int page = info.key_exp[c0 / 64], v = info.value_exp & kApart ? info.value_of[c0 + lane] : info.value_exp;
+        const unsigned bad = __ballot_sync(0xFFFFFFFFu, v == kBad);
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const int ke = page & kApart ? kw[i / 4] >> (8 * (i & 3)) & 255 : page;
-            const int ve = info.value_exp & kApart ? vw[i / 4] >> (8 * (i & 3)) & 255 : info.value_exp;
-            // 2^(ke - kOffset) is a float up to 127: 2^7 of it goes to the row's factor
-            x[i] = i < n ? __uint_as_float(r[i]) * (row_scale * 128.0f) * __int_as_float((ke - kOffset - 7 + 127) << 23) : -INFINITY;
-            e[i] = (float)(ve - kOffset);
-            bad |= i < n && ve == kBad;
-            mx = fmaxf(mx, x[i]);
-            mp = fmaxf(mp, x[i] + e[i]);
+        for (int i = 0; i < 32; i++) e[i] = __shfl_sync(0xFFFFFFFFu, (float)(v - kOffset), i);
+        tmem_ld_wait32(r);
+        float f = row_scale * __int_as_float(((page & (kApart - 1)) - kOffset + 127) << 23);
+        if (page & kApart) {
+            // a token's power is a float's up to 2^127: 2^7 of it goes to the row's factor
+            f = row_scale * 128.0f;
+            const float own = __int_as_float((info.key_of[c0 + lane] - kOffset - 7 + 127) << 23);
+#pragma unroll
+            for (int i = 0; i < 32; i++) r[i] = __float_as_uint(__uint_as_float(r[i]) * __shfl_sync(0xFFFFFFFFu, own, i));
+        }
+        const int n = info.there >> (c0 / 64) & 1 ? seen - c0 : 0;
+        float mx = -INFINITY, mp = -INFINITY;   // largest score, largest score of a P
+#pragma unroll
+        for (int i = 0; i < 32; i++) {
+            const float x = i < n ? f * __uint_as_float(r[i]) : -INFINITY;
+            mx = fmaxf(mx, x);
+            mp = fmaxf(mp, x + e[i]);
         }
         const bool far = mx > row.m + 8.0f || mp - row.m + (float)row.off > 14.0f;
         if (__any_sync(0xFFFFFFFFu, far)) {
             const Moved by = far ? move_row(mx, mp, row) : Moved{1.0f, 1.0f};
             rescale<D>(s_tmem, o_tmem, c0, first, by.o);
         }
-        const float ref = row.m == -INFINITY ? 0.0f : row.m;
-        float sum = bad ? __int_as_float(0x7FFFFFFF) : 0.0f;
-        uint32_t pk[8];
+        const float nm = row.m == -INFINITY ? 0.0f : -row.m, np = nm + (float)row.off;
+        float sum[2] = {0.0f, 0.0f};
+        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            sum += exp2_fast(x[i] - ref) + exp2_fast(x[i + 1] - ref);
-            pk[i / 2] = pack_f16(exp2_fast(x[i] - ref + (e[i] + (float)row.off)), exp2_fast(x[i + 1] - ref + (e[i + 1] + (float)row.off)));
+        for (int i = 0; i < 32; i += 2) {
+            float p[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const float x = __uint_as_float(r[i + k]), one = exp2_fast(f * x + nm);
+                p[k] = exp2_fast(f * x + np + e[i + k]);
+                sum[k] += i + k < n ? one : 0.0f;
+                p[k] = i + k < n ? p[k] : 0.0f;
+            }
+            pk[i / 2] = pack_f16(p[0], p[1]);
         }
-        row.l = add2(row.l, pair2(sum, 0.0f));
-        tmem_st8(s_tmem + c0 / 2, pk);
+        if (n > 0 && (bad & (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u)) != 0) sum[0] = __int_as_float(0x7FFFFFFF);
+        row.l = add2(row.l, pair2(sum[0], sum[1]));
+        tmem_st16(s_tmem + c0 / 2, pk);
     }
     return row;
 }
@@ -550,17 +565,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             tc_fence_after();
             const StepInfo &info = bar->info[slot];
             if (++slot == kInfoSlots) slot = 0, lap ^= 1;
-            const int there = info.there, t0 = j * kKeys;
+            const int4 what = *reinterpret_cast<const int4 *>(info.key_exp);  // key_exp, value_exp, there
+            const int there = what.w, t0 = j * kKeys;
             const int seen = min(max(last - t0 + 1, 0), kKeys);
-            const int k0 = info.key_exp[0], k1 = info.key_exp[1], v = info.value_exp, ve = v - kOffset;
-            // a row whose P would all be far below or above its largest takes the step token by token too
-            const bool far = row.m != -INFINITY && (ve + row.off < -40 || ve + row.off > 100);
-            if (__any_sync(0xFFFFFFFFu, far || (k0 | k1 | v) & kApart)) {
-                row = step_apart<D>(s_tmem, o_tmem, row_scale, info, seen, j == 0, row);
-            } else {
+            const int k0 = what.x, k1 = what.y, v = what.z, ve = v - kOffset;
+            // (token by token too where a row's P would all be below 2^-40 or above 2^100)
+            const bool far = row.m != -INFINITY && (unsigned)(ve + row.off + 40) > 140u;
+            if (!__any_sync(0xFFFFFFFFu, far || (k0 | k1 | v) & kApart)) {
                 const float f0 = row_scale * __int_as_float((k0 - kOffset + 127) << 23), f1 = row_scale * __int_as_float((k1 - kOffset + 127) << 23);
                 if (there == 3 && t0 + kKeys - 1 <= last_min) step_probs<D, false>(s_tmem, o_tmem, f0, f1, ve, seen, there, j == 0, row);
                 else step_probs<D, true>(s_tmem, o_tmem, f0, f1, ve, seen, there, j == 0, row);
+            } else {
+                row = step_apart<D>(s_tmem, o_tmem, row_scale, info, seen, j == 0, row);
             }
             tmem_st_wait();
             tc_fence_before();

@@ -18,8 +18,8 @@ namespace {
 // short sequences load the machine alike (and as few runs as that takes: fewer parts to join); row tiles
 // that a run does not hold whole go to the workspace and a second kernel joins their parts in the order of
 // the runs (no atomics: results do not depend on timing).  Few row tiles of few pages go to a cluster each
-// instead, which joins its warps' parts in shared memory.  A warp works alone: it copies its pages into its own ring (a page's keys and values are one
-// contiguous block: one bulk copy), and no other warp waits for it.
+// instead, which joins its warps' parts in shared memory.  A warp works alone: it copies its pages into its
+// own ring (a page's keys and values are one contiguous block: one bulk copy), and no other warp waits for it.
 // The product is S^T = K q^T, 16 tokens by 8 rows: the 8-wide side carries the few rows, so 4 query heads
 // per key/value head fill half of the instruction instead of a quarter.
 // Decoding is what bounds it next (integer instructions, half of an SM's rate): a code's four bits at the
@@ -391,186 +391,186 @@ __global__ void __launch_bounds__(kFewThreads, (Few<D, NT>::kCtas)) attn_few_ker
                 for (int t = 0; t < NT; t++) ones[t][0] = ones[t][1] = ones[t][2] = ones[t][3] = 0.0f;
 #pragma unroll 1
                 for (int q0 = 0; q0 < 4; q0 += kTiles) {
-                float x[kTiles][NT][4];                       // scores of tiles of 16 tokens
+                    float x[kTiles][NT][4];                       // scores of tiles of 16 tokens
 #pragma unroll
-                for (int qi = 0; qi < kTiles; qi++) {
-                    const int q = q0 + qi;
-                    const int ta = 16 * q + tok_r;            // rows r, r + 8 of the tile
-                    uint32_t kw[2][WK];
+                    for (int qi = 0; qi < kTiles; qi++) {
+                        const int q = q0 + qi;
+                        const int ta = 16 * q + tok_r;            // rows r, r + 8 of the tile
+                        uint32_t kw[2][WK];
 #pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const uint8_t *src = kb + (ta + 8 * i) * Kv4<D>::kRow + c * (D / 8);
-                        if (D == 64) {
-                            const uint2 u = *reinterpret_cast<const uint2 *>(src);
-                            kw[i][0] = u.x, kw[i][1] = u.y;
-                        } else {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(src);
-                            kw[i][0] = u.x, kw[i][1] = u.y;
-                            kw[i][WK - 2] = u.z, kw[i][WK - 1] = u.w;
+                        for (int i = 0; i < 2; i++) {
+                            const uint8_t *src = kb + (ta + 8 * i) * Kv4<D>::kRow + c * (D / 8);
+                            if (D == 64) {
+                                const uint2 u = *reinterpret_cast<const uint2 *>(src);
+                                kw[i][0] = u.x, kw[i][1] = u.y;
+                            } else {
+                                const uint4 u = *reinterpret_cast<const uint4 *>(src);
+                                kw[i][0] = u.x, kw[i][1] = u.y;
+                                kw[i][WK - 2] = u.z, kw[i][WK - 1] = u.w;
+                            }
                         }
+                        const uint32_t *ksm = reinterpret_cast<const uint32_t *>(kb + Kv4<D>::kCodes) + ta;
+                        const uint32_t kp[2] = {ksm[0], ksm[8]};
+#pragma unroll
+                        for (int t = 0; t < NT; t++) x[qi][t][0] = x[qi][t][1] = x[qi][t][2] = x[qi][t][3] = 0.0f;
+#pragma unroll
+                        for (int w = 0; w < WK; w++)
+#pragma unroll
+                            for (int k = 0; k < 2; k++) {
+                                const uint32_t u0 = kw[0][w] >> (8 * k), u1 = kw[1][w] >> (8 * k);
+                                const uint32_t a[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
+#pragma unroll
+                                for (int t = 0; t < NT; t++) mma_f16(x[qi][t], a, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
+                            }
+#pragma unroll
+                        for (int t = 0; t < NT; t++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++)
+#pragma unroll
+                                for (int j = 0; j < 2; j++)
+                                    x[qi][t][2 * i + j] = kv4_step(kp[i]) * x[qi][t][2 * i + j] + kv4_low(kp[i]) * qsum[t][j];
                     }
-                    const uint32_t *ksm = reinterpret_cast<const uint32_t *>(kb + Kv4<D>::kCodes) + ta;
-                    const uint32_t kp[2] = {ksm[0], ksm[8]};
-#pragma unroll
-                    for (int t = 0; t < NT; t++) x[qi][t][0] = x[qi][t][1] = x[qi][t][2] = x[qi][t][3] = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < WK; w++)
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const uint32_t u0 = kw[0][w] >> (8 * k), u1 = kw[1][w] >> (8 * k);
-                            const uint32_t a[4] = {u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x00F000F0u};
-#pragma unroll
-                            for (int t = 0; t < NT; t++) mma_f16(x[qi][t], a, qf[t][2 * w + k][0], qf[t][2 * w + k][1]);
-                        }
-#pragma unroll
-                    for (int t = 0; t < NT; t++)
-#pragma unroll
-                        for (int i = 0; i < 2; i++)
-#pragma unroll
-                            for (int j = 0; j < 2; j++)
-                                x[qi][t][2 * i + j] = kv4_step(kp[i]) * x[qi][t][2 * i + j] + kv4_low(kp[i]) * qsum[t][j];
-                }
-                float sv[kTiles][2], mv[kTiles][2];           // steps and centres of the values
-#pragma unroll
-                for (int qi = 0; qi < kTiles; qi++)
-#pragma unroll
-                    for (int i = 0; i < 2; i++) {
-                        const uint32_t vp = reinterpret_cast<const uint32_t *>(vb + Kv4<D>::kCodes)[16 * (q0 + qi) + tok_r + 8 * i];
-                        sv[qi][i] = kv4_step(vp);
-                        mv[qi][i] = kv4_low(vp) + 8.0f * sv[qi][i];
-                    }
-                if (!whole) {
-                    // A token that a row does not see may hold anything: its probability is 2^-inf, and a step or
-                    // centre that is not a number goes to the score of the rows that do see it.
+                    float sv[kTiles][2], mv[kTiles][2];           // steps and centres of the values
 #pragma unroll
                     for (int qi = 0; qi < kTiles; qi++)
 #pragma unroll
                         for (int i = 0; i < 2; i++) {
-                            const int tok = t0 + 16 * (q0 + qi) + tok_r + 8 * i;
-                            const bool bad = !(fabsf(sv[qi][i]) < INFINITY && fabsf(mv[qi][i]) < INFINITY);
-                            if (bad || tok > last_max) sv[qi][i] = mv[qi][i] = 0.0f;
+                            const uint32_t vp = reinterpret_cast<const uint32_t *>(vb + Kv4<D>::kCodes)[16 * (q0 + qi) + tok_r + 8 * i];
+                            sv[qi][i] = kv4_step(vp);
+                            mv[qi][i] = kv4_low(vp) + 8.0f * sv[qi][i];
+                        }
+                    if (!whole) {
+                        // A token that a row does not see may hold anything: its probability is 2^-inf, and a step or
+                        // centre that is not a number goes to the score of the rows that do see it.
 #pragma unroll
-                            for (int t = 0; t < NT; t++)
+                        for (int qi = 0; qi < kTiles; qi++)
 #pragma unroll
-                                for (int j = 0; j < 2; j++) {
-                                    if (bad) x[qi][t][2 * i + j] = __int_as_float(0x7FFFFFFF);
-                                    if (tok > last[t][j]) x[qi][t][2 * i + j] = -INFINITY;
+                            for (int i = 0; i < 2; i++) {
+                                const int tok = t0 + 16 * (q0 + qi) + tok_r + 8 * i;
+                                const bool bad = !(fabsf(sv[qi][i]) < INFINITY && fabsf(mv[qi][i]) < INFINITY);
+                                if (bad || tok > last_max) sv[qi][i] = mv[qi][i] = 0.0f;
+#pragma unroll
+                                for (int t = 0; t < NT; t++)
+#pragma unroll
+                                    for (int j = 0; j < 2; j++) {
+                                        if (bad) x[qi][t][2 * i + j] = __int_as_float(0x7FFFFFFF);
+                                        if (tok > last[t][j]) x[qi][t][2 * i + j] = -INFINITY;
+                                    }
+                            }
+                    }
+                    uint32_t pb[kTiles][NT][2];
+                    f2 sum[NT], csum[NT];
+                    // References and powers move only when a lane's sums outgrow them: most pages skip the shuffles and
+                    // the rescaling.
+                    for (bool moved = false;; moved = true) {
+                        f2 most[NT];
+#pragma unroll
+                        for (int t = 0; t < NT; t++) sum[t] = csum[t] = most[t] = pair2(0.0f, 0.0f);
+#pragma unroll
+                        for (int qi = 0; qi < kTiles; qi++)
+#pragma unroll
+                            for (int i = 0; i < 2; i++) {
+                                const f2 s2 = pair2(sv[qi][i], sv[qi][i]), m2 = pair2(mv[qi][i], mv[qi][i]);
+#pragma unroll
+                                for (int t = 0; t < NT; t++) {
+                                    float a, b;
+                                    split2(fma2(pair2(x[qi][t][2 * i], x[qi][t][2 * i + 1]), sc[t], nref[t]), a, b);
+                                    const f2 pr = pair2(exp2_fast(a), exp2_fast(b));
+                                    const f2 ps = mul2(mul2(pr, s2), down[t]);
+                                    sum[t] = add2(sum[t], pr);
+                                    csum[t] = fma2(pr, m2, csum[t]);
+                                    most[t] = add2(most[t], ps);
+                                    split2(ps, a, b);
+                                    pb[qi][t][i] = pack_f16(a, b);
                                 }
-                        }
-                }
-                uint32_t pb[kTiles][NT][2];
-                f2 sum[NT], csum[NT];
-                // References and powers move only when a lane's sums outgrow them: most pages skip the shuffles and
-                // the rescaling.
-                for (bool moved = false;; moved = true) {
-                    f2 most[NT];
-#pragma unroll
-                    for (int t = 0; t < NT; t++) sum[t] = csum[t] = most[t] = pair2(0.0f, 0.0f);
-#pragma unroll
-                    for (int qi = 0; qi < kTiles; qi++)
-#pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const f2 s2 = pair2(sv[qi][i], sv[qi][i]), m2 = pair2(mv[qi][i], mv[qi][i]);
-#pragma unroll
-                            for (int t = 0; t < NT; t++) {
-                                float a, b;
-                                split2(fma2(pair2(x[qi][t][2 * i], x[qi][t][2 * i + 1]), sc[t], nref[t]), a, b);
-                                const f2 pr = pair2(exp2_fast(a), exp2_fast(b));
-                                const f2 ps = mul2(mul2(pr, s2), down[t]);
-                                sum[t] = add2(sum[t], pr);
-                                csum[t] = fma2(pr, m2, csum[t]);
-                                most[t] = add2(most[t], ps);
-                                split2(ps, a, b);
-                                pb[qi][t][i] = pack_f16(a, b);
                             }
+                        bool grow = false;
+#pragma unroll
+                        for (int t = 0; t < NT; t++) {
+                            float a, b;
+                            split2(sum[t], a, b);
+                            grow |= fmaxf(a, b) > kPTop;
+                            split2(most[t], a, b);
+                            grow |= fmaxf(a, b) > kPsTop;
                         }
-                    bool grow = false;
+                        // once is enough (a row of nothing but NaN has no reference after it either)
+                        if (moved || !__any_sync(0xFFFFFFFFu, grow)) break;
+#pragma unroll
+                        for (int t = 0; t < NT; t++) {
+                            float scale[2], old[2], d[2], f[2], fo[2];
+                            split2(sc[t], scale[0], scale[1]);
+                            split2(nref[t], old[0], old[1]);
+                            split2(down[t], d[0], d[1]);
+#pragma unroll
+                            for (int j = 0; j < 2; j++) {
+                                // largest score, and largest score of p s (up to a factor of two)
+                                float mx = -INFINITY, ms = -INFINITY;
+#pragma unroll
+                                for (int k = 0; k < 2 * kTiles; k++) {
+                                    const float y = x[k >> 1][t][2 * (k & 1) + j] * scale[j];
+                                    mx = fmaxf(mx, y);
+                                    ms = fmaxf(ms, y + (float)((int)(__float_as_uint(sv[k >> 1][k & 1]) >> 23 & 255) - 126));
+                                }
+#pragma unroll
+                                for (int k = 4; k < 32; k <<= 1) {
+                                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
+                                    ms = fmaxf(ms, __shfl_xor_sync(0xFFFFFFFFu, ms, k));
+                                }
+                                const float ref = fmaxf(-old[j], ceilf(mx) + (float)kDown), by = -old[j] - ref;   // by <= 0
+                                // what is summed already needs no more than its power, by lower
+                                const float ve = (float)(127 - (int)(__float_as_uint(d[j]) >> 23));
+                                const float to = fmaxf(fmaxf(ve + by, ceilf(ms - ref) - (float)kUp), -126.0f);
+                                old[j] = -ref;
+                                d[j] = __int_as_float((127 - (int)to) << 23);
+                                f[j] = exp2_fast(by);
+                                fo[j] = exp2_fast(ve + by - to);
+                                ones[t][j] *= fo[j];
+#pragma unroll
+                                for (int i = 0; i < MT; i++) {
+                                    o[t][i][j] *= fo[j];
+                                    o[t][i][2 + j] *= fo[j];
+                                }
+                            }
+                            nref[t] = pair2(old[0], old[1]);
+                            down[t] = pair2(d[0], d[1]);
+                            l[t] = mul2(l[t], pair2(f[0], f[1]));
+                            corr[t] = mul2(corr[t], pair2(f[0], f[1]));
+                        }
+                    }
 #pragma unroll
                     for (int t = 0; t < NT; t++) {
-                        float a, b;
-                        split2(sum[t], a, b);
-                        grow |= fmaxf(a, b) > kPTop;
-                        split2(most[t], a, b);
-                        grow |= fmaxf(a, b) > kPsTop;
+                        l[t] = add2(l[t], sum[t]);
+                        corr[t] = add2(corr[t], csum[t]);
                     }
-                    // once is enough (a row of nothing but NaN has no reference after it either)
-                    if (moved || !__any_sync(0xFFFFFFFFu, grow)) break;
 #pragma unroll
-                    for (int t = 0; t < NT; t++) {
-                        float scale[2], old[2], d[2], f[2], fo[2];
-                        split2(sc[t], scale[0], scale[1]);
-                        split2(nref[t], old[0], old[1]);
-                        split2(down[t], d[0], d[1]);
+                    for (int qi = 0; qi < kTiles; qi++) {
+                        const int q = q0 + qi;
 #pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            // largest score, and largest score of p s (up to a factor of two)
-                            float mx = -INFINITY, ms = -INFINITY;
+                        for (int t = 0; t < NT; t++)
 #pragma unroll
-                            for (int k = 0; k < 2 * kTiles; k++) {
-                                const float y = x[k >> 1][t][2 * (k & 1) + j] * scale[j];
-                                mx = fmaxf(mx, y);
-                                ms = fmaxf(ms, y + (float)((int)(__float_as_uint(sv[k >> 1][k & 1]) >> 23 & 255) - 126));
-                            }
+                            for (int i = 0; i < 2; i++) pb[qi][t][i] = transpose8x8(pb[qi][t][i]);
+                        // values: lane (r, c) holds word(s) r of four tokens; a pair of tokens per register
 #pragma unroll
-                            for (int k = 4; k < 32; k <<= 1) {
-                                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
-                                ms = fmaxf(ms, __shfl_xor_sync(0xFFFFFFFFu, ms, k));
-                            }
-                            const float ref = fmaxf(-old[j], ceilf(mx) + (float)kDown), by = -old[j] - ref;   // by <= 0
-                            // what is summed already needs no more than its power, by lower
-                            const float ve = (float)(127 - (int)(__float_as_uint(d[j]) >> 23));
-                            const float to = fmaxf(fmaxf(ve + by, ceilf(ms - ref) - (float)kUp), -126.0f);
-                            old[j] = -ref;
-                            d[j] = __int_as_float((127 - (int)to) << 23);
-                            f[j] = exp2_fast(by);
-                            fo[j] = exp2_fast(ve + by - to);
-                            ones[t][j] *= fo[j];
+                        for (int w = 0; w < D / 64; w++) {
+                            const uint8_t *src = vb + 16 * q * Kv4<D>::kRow + (r * (D / 64) + w) * 4;
+                            const uint32_t w0 = *reinterpret_cast<const uint32_t *>(src + tok_v0 * Kv4<D>::kRow);
+                            const uint32_t w1 = *reinterpret_cast<const uint32_t *>(src + tok_v1 * Kv4<D>::kRow);
+                            const uint32_t w2 = *reinterpret_cast<const uint32_t *>(src + (tok_v0 + 8) * Kv4<D>::kRow);
+                            const uint32_t w3 = *reinterpret_cast<const uint32_t *>(src + (tok_v1 + 8) * Kv4<D>::kRow);
+                            const uint32_t al = prmt(w0, w1, 0x5410), ah = prmt(w0, w1, 0x7632);
+                            const uint32_t bl = prmt(w2, w3, 0x5410), bh = prmt(w2, w3, 0x7632);
 #pragma unroll
-                            for (int i = 0; i < MT; i++) {
-                                o[t][i][j] *= fo[j];
-                                o[t][i][2 + j] *= fo[j];
+                            for (int i = 0; i < 4; i++) {
+                                const uint32_t mask = i & 1 ? 0x00F000F0u : 0x000F000Fu;
+                                const int sh = 8 * (i >> 1);
+                                const uint32_t a[4] = {(al >> sh) & mask, (ah >> sh) & mask, (bl >> sh) & mask, (bh >> sh) & mask};
+#pragma unroll
+                                for (int t = 0; t < NT; t++) mma_f16(o[t][4 * w + i], a, pb[qi][t][0], pb[qi][t][1]);
                             }
                         }
-                        nref[t] = pair2(old[0], old[1]);
-                        down[t] = pair2(d[0], d[1]);
-                        l[t] = mul2(l[t], pair2(f[0], f[1]));
-                        corr[t] = mul2(corr[t], pair2(f[0], f[1]));
+#pragma unroll
+                        for (int t = 0; t < NT; t++) mma_f16(ones[t], a1, pb[qi][t][0], pb[qi][t][1]);
                     }
-                }
-#pragma unroll
-                for (int t = 0; t < NT; t++) {
-                    l[t] = add2(l[t], sum[t]);
-                    corr[t] = add2(corr[t], csum[t]);
-                }
-#pragma unroll
-                for (int qi = 0; qi < kTiles; qi++) {
-                    const int q = q0 + qi;
-#pragma unroll
-                    for (int t = 0; t < NT; t++)
-#pragma unroll
-                        for (int i = 0; i < 2; i++) pb[qi][t][i] = transpose8x8(pb[qi][t][i]);
-                    // values: lane (r, c) holds word(s) r of four tokens; a pair of tokens per register
-#pragma unroll
-                    for (int w = 0; w < D / 64; w++) {
-                        const uint8_t *src = vb + 16 * q * Kv4<D>::kRow + (r * (D / 64) + w) * 4;
-                        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(src + tok_v0 * Kv4<D>::kRow);
-                        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(src + tok_v1 * Kv4<D>::kRow);
-                        const uint32_t w2 = *reinterpret_cast<const uint32_t *>(src + (tok_v0 + 8) * Kv4<D>::kRow);
-                        const uint32_t w3 = *reinterpret_cast<const uint32_t *>(src + (tok_v1 + 8) * Kv4<D>::kRow);
-                        const uint32_t al = prmt(w0, w1, 0x5410), ah = prmt(w0, w1, 0x7632);
-                        const uint32_t bl = prmt(w2, w3, 0x5410), bh = prmt(w2, w3, 0x7632);
-#pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const uint32_t mask = i & 1 ? 0x00F000F0u : 0x000F000Fu;
-                            const int sh = 8 * (i >> 1);
-                            const uint32_t a[4] = {(al >> sh) & mask, (ah >> sh) & mask, (bl >> sh) & mask, (bh >> sh) & mask};
-#pragma unroll
-                            for (int t = 0; t < NT; t++) mma_f16(o[t][4 * w + i], a, pb[qi][t][0], pb[qi][t][1]);
-                        }
-                    }
-#pragma unroll
-                    for (int t = 0; t < NT; t++) mma_f16(ones[t], a1, pb[qi][t][0], pb[qi][t][1]);
-                }
                 }
                 // The tensor cores' sums round towards zero, and a long sum of codes 0 .. 15 drifts (32,768 tokens
                 // came out at twice the error of a bf16 result): the page's 8 sum(p s) comes off again, so that the

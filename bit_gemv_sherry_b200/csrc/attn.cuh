@@ -29,7 +29,7 @@ struct AttnParams {
     unsigned int *err;
 };
 
-// Sequences of more than p.few_rows rows: 128-row tiles on the tensor cores.
+// Sequences of more than p.few_rows rows: 256 rows a CTA, two tiles of 128 on the tensor cores.
 sherry_status attn_tile_launch(const AttnParams &p, int D, cudaStream_t stream);
 
 __device__ __forceinline__ float exp2_fast(float x) {

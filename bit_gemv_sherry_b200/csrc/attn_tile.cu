@@ -5,9 +5,9 @@
 // value serves both (and all query heads of the group: a row is a new token and a query head).
 // Per step of 128 tokens:
 //     S = Q K^T            fp16 operands, K-major, in shared memory; S (fp32) in tensor memory
-//     P = fp16(2^(f S - m))  back into S's tensor memory, the A operand of
+//     P = fp16(2^(f S - m + e))  back into S's tensor memory, the A operand of
 //     O += P V             V transposed to [D][tokens], so that both operands are K-major
-// and l += sum p in fp32;  out = O / l.
+// and l += sum 2^(f S - m) in fp32;  out = O 2^-off / l (e and off: below).
 // Precision: decoded values are m + s c rounded once to fp16 (11 bits; bf16's 8 would cost the
 // scores of a peaked softmax several percent), after a division by a power of two that brings the
 // largest to about 2^-6: there a code's bits are themselves an fp16, c 2^-24, and one FMA makes the
@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
             // (token by token too where a row's P would all be below 2^-40 or above 2^100)
             const bool far = row.m != -INFINITY && (unsigned)(ve + row.off + 40) > 140u;
             if (!__any_sync(0xFFFFFFFFu, far || (k0 | k1 | v) & kApart)) {
-                const float f0 = row_scale * __int_as_float((k0 - kOffset + 127) << 23), f1 = row_scale * __int_as_float((k1 - kOffset + 127) << 23);
+                const float f0 = row_scale * __int_as_float((k0 - kOffset + 127) << 23);
+                const float f1 = row_scale * __int_as_float((k1 - kOffset + 127) << 23);
                 if (there == 3 && t0 + kKeys - 1 <= last_min) step_probs<D, false>(s_tmem, o_tmem, f0, f1, ve, seen, there, j == 0, row);
                 else step_probs<D, true>(s_tmem, o_tmem, f0, f1, ve, seen, there, j == 0, row);
             } else {
@@ -617,190 +618,190 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
     } else if (warp < 12) {
         regs_down<96>();
         if (warp < 10) {
-        // ---------------- keys: a warp per page, two tokens per thread ----------------
-        const int k = warp - 8;
-        for (int j = 0, slot = 0; j < steps; j++) {
-            const int s = j & 1;
-            if (!warp_wait(&bar->raw_full[s], (j >> 1) & 1, abort, p.err, limit)) break;
-            const uint8_t *blk = raw + (2 * s + k) * T::kPage;
-            const int there = bar->there[s];
-            // tokens past the last that a row of this CTA sees may hold anything: they count as zeros
-            const int in = there >> k & 1 ? keys - j * kKeys - k * SHERRY_KV4_PAGE : 0;
-            const uint32_t *pairs = reinterpret_cast<const uint32_t *>(blk + Kv4<D>::kCodes);
-            const uint32_t sm[2] = {lane < in ? pairs[lane] : 0u, lane + 32 < in ? pairs[lane + 32] : 0u};
-            const float size[2] = {pair_most(sm[0]), pair_most(sm[1])};
-            auto some = [](float v) { return v == 0.0f ? INFINITY : v; };
-            int shared = shared_exp(fminf(some(size[0]), some(size[1])), fmaxf(size[0], size[1]));
-            if (shared > kOffset + kMostExp) shared |= kApart;
-            const int e = (shared & (kApart - 1)) - kOffset;
-            int own[2] = {e, e};
-            if (!warp_wait(&bar->k_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
-            // The slot is free: the products of step j - 2 are complete, and their last half was issued after the
-            // softmax of step j - 3.
-            StepInfo &info = bar->info[slot];
-            if (lane == 0) {
-                info.key_exp[k] = shared;
-                if (k == 0) info.there = there;
-            }
-            if (shared & kApart) {
-                own[0] = exp_for(size[0]), own[1] = exp_for(size[1]);
-                info.key_of[SHERRY_KV4_PAGE * k + lane] = (uint8_t)(own[0] + kOffset);
-                info.key_of[SHERRY_KV4_PAGE * k + lane + 32] = (uint8_t)(own[1] + kOffset);
-            }
-            warp_arrive(&bar->info_full[slot]);
-            if (++slot == kInfoSlots) slot = 0;
+            // ---------------- keys: a warp per page, two tokens per thread ----------------
+            const int k = warp - 8;
+            for (int j = 0, slot = 0; j < steps; j++) {
+                const int s = j & 1;
+                if (!warp_wait(&bar->raw_full[s], (j >> 1) & 1, abort, p.err, limit)) break;
+                const uint8_t *blk = raw + (2 * s + k) * T::kPage;
+                const int there = bar->there[s];
+                // tokens past the last that a row of this CTA sees may hold anything: they count as zeros
+                const int in = there >> k & 1 ? keys - j * kKeys - k * SHERRY_KV4_PAGE : 0;
+                const uint32_t *pairs = reinterpret_cast<const uint32_t *>(blk + Kv4<D>::kCodes);
+                const uint32_t sm[2] = {lane < in ? pairs[lane] : 0u, lane + 32 < in ? pairs[lane + 32] : 0u};
+                const float size[2] = {pair_most(sm[0]), pair_most(sm[1])};
+                auto some = [](float v) { return v == 0.0f ? INFINITY : v; };
+                int shared = shared_exp(fminf(some(size[0]), some(size[1])), fmaxf(size[0], size[1]));
+                if (shared > kOffset + kMostExp) shared |= kApart;
+                const int e = (shared & (kApart - 1)) - kOffset;
+                int own[2] = {e, e};
+                if (!warp_wait(&bar->k_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
+                // The slot is free: the products of step j - 2 are complete, and their last half was issued after the
+                // softmax of step j - 3.
+                StepInfo &info = bar->info[slot];
+                if (lane == 0) {
+                    info.key_exp[k] = shared;
+                    if (k == 0) info.there = there;
+                }
+                if (shared & kApart) {
+                    own[0] = exp_for(size[0]), own[1] = exp_for(size[1]);
+                    info.key_of[SHERRY_KV4_PAGE * k + lane] = (uint8_t)(own[0] + kOffset);
+                    info.key_of[SHERRY_KV4_PAGE * k + lane + 32] = (uint8_t)(own[1] + kOffset);
+                }
+                warp_arrive(&bar->info_full[slot]);
+                if (++slot == kInfoSlots) slot = 0;
 #pragma unroll 1
-            for (int t = 0; t < 2; t++) {
-                const float down = pow2(-own[t]);
-                const int row = lane + 32 * t, tok = SHERRY_KV4_PAGE * k + row;
-                const float st = kv4_step(sm[t]) * down, lo = kv4_low(sm[t]) * down;
-                const uint32_t s0 = pack_f16(st * 16777216.0f, st * 16777216.0f), s1 = pack_f16(st * 1048576.0f, st * 1048576.0f);
-                const uint32_t m2 = pack_f16(lo, lo);
-                const uint8_t *src = blk + row * Kv4<D>::kRow;
-                uint8_t *dst = sk + s * T::kOp + tok * 128;
+                for (int t = 0; t < 2; t++) {
+                    const float down = pow2(-own[t]);
+                    const int row = lane + 32 * t, tok = SHERRY_KV4_PAGE * k + row;
+                    const float st = kv4_step(sm[t]) * down, lo = kv4_low(sm[t]) * down;
+                    const uint32_t s0 = pack_f16(st * 16777216.0f, st * 16777216.0f), s1 = pack_f16(st * 1048576.0f, st * 1048576.0f);
+                    const uint32_t m2 = pack_f16(lo, lo);
+                    const uint8_t *src = blk + row * Kv4<D>::kRow;
+                    uint8_t *dst = sk + s * T::kOp + tok * 128;
 #pragma unroll 2
-                for (int q = 0; q < D / 32; q++) {
-                    // 16-byte pieces of a row in an order that keeps eight rows out of each other's banks
-                    const int qq = (q + (D == 128 ? row >> 1 : row >> 2)) & (D / 32 - 1);
-                    uint4 u = *reinterpret_cast<const uint4 *>(src + 16 * qq);
-                    if (row >= in) u = make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-                    uint8_t *half = dst + (qq / 2) * (kKeys * 128);
+                    for (int q = 0; q < D / 32; q++) {
+                        // 16-byte pieces of a row in an order that keeps eight rows out of each other's banks
+                        const int qq = (q + (D == 128 ? row >> 1 : row >> 2)) & (D / 32 - 1);
+                        uint4 u = *reinterpret_cast<const uint4 *>(src + 16 * qq);
+                        if (row >= in) u = make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                        uint8_t *half = dst + (qq / 2) * (kKeys * 128);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int c = (4 * qq + i) & 7;  // 8-element chunk of the 128-byte row
-                        const uint32_t y = x[i] >> 8;
-                        *reinterpret_cast<uint4 *>(half + ((c ^ (tok & 7)) << 4)) =
-                            make_uint4(value_pair<0x000F000F>(x[i], s0, m2), value_pair<0x00F000F0>(x[i], s1, m2),
-                                       value_pair<0x000F000F>(y, s0, m2), value_pair<0x00F000F0>(y, s1, m2));
+                        for (int i = 0; i < 4; i++) {
+                            const int c = (4 * qq + i) & 7;  // 8-element chunk of the 128-byte row
+                            const uint32_t y = x[i] >> 8;
+                            *reinterpret_cast<uint4 *>(half + ((c ^ (tok & 7)) << 4)) =
+                                make_uint4(value_pair<0x000F000F>(x[i], s0, m2), value_pair<0x00F000F0>(x[i], s1, m2),
+                                           value_pair<0x000F000F>(y, s0, m2), value_pair<0x00F000F0>(y, s1, m2));
+                        }
                     }
                 }
+                fence_proxy_async_smem();
+                warp_arrive(&bar->k_full[s]);
+                warp_arrive(&bar->raw_empty[s]);
             }
-            fence_proxy_async_smem();
-            warp_arrive(&bar->k_full[s]);
-            warp_arrive(&bar->raw_empty[s]);
-        }
         } else {
-        // ---------------- values: a warp per page, eight tokens per thread, transposed ----------------
-        const int k = warp - 10;
-        const int grp = lane & 7, qd = lane >> 3;  // tokens 8 grp ... of the page, word qd of each four
-        const int odd = grp & 1;                   // these read the tokens of a pair in the other order, for the banks
-        for (int j = 0, slot = 0; j < steps; j++) {
-            const int s = j & 1;
-            if (!warp_wait(&bar->raw_full[s], (j >> 1) & 1, abort, p.err, limit)) break;
-            const int there = bar->there[s];
-            const uint8_t *blk = raw + 2 * s * T::kPage + Kv4<D>::kBlock;  // the first page's values
-            uint32_t pair[4];                                              // of tokens lane + 32 i of the step
-            float least = INFINITY, most = 0.0f;
+            // ---------------- values: a warp per page, eight tokens per thread, transposed ----------------
+            const int k = warp - 10;
+            const int grp = lane & 7, qd = lane >> 3;  // tokens 8 grp ... of the page, word qd of each four
+            const int odd = grp & 1;                   // these read the tokens of a pair in the other order, for the banks
+            for (int j = 0, slot = 0; j < steps; j++) {
+                const int s = j & 1;
+                if (!warp_wait(&bar->raw_full[s], (j >> 1) & 1, abort, p.err, limit)) break;
+                const int there = bar->there[s];
+                const uint8_t *blk = raw + 2 * s * T::kPage + Kv4<D>::kBlock;  // the first page's values
+                uint32_t pair[4];                                              // of tokens lane + 32 i of the step
+                float least = INFINITY, most = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const bool in = (there >> (i / 2) & 1) && j * kKeys + lane + 32 * i < keys;
-                pair[i] = in ? reinterpret_cast<const uint32_t *>(blk + (i / 2) * T::kPage + Kv4<D>::kCodes)[lane + 32 * (i & 1)] : 0u;
-                const float size = pair_most(pair[i]);
-                least = fminf(least, size != 0.0f ? size : pair_bad(pair[i]) ? 0.0f : INFINITY);
-                most = fmaxf(most, size);
-            }
-            const int shared = shared_exp(least, most);
-            const int ve = (shared & (kApart - 1)) - kOffset;
-            const bool apart = shared & kApart;
-            blk += k * T::kPage;
-            const int in = there >> k & 1 ? keys - j * kKeys - k * SHERRY_KV4_PAGE - 8 * grp : 0;  // tokens of the eight that are there
-            uint32_t s0[4], s1[4], m2[4];
-            const float down = pow2(-ve);
-#pragma unroll
-            for (int t = 0; t < 4; t++) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(blk + Kv4<D>::kCodes + 4 * (8 * grp + 2 * t));
-                uint32_t a = 2 * t < in ? u.x : 0u, b = 2 * t + 1 < in ? u.y : 0u;
-                float da = down, db = down;
-                if (apart) {
-                    if (pair_bad(a)) a = 0u;
-                    if (pair_bad(b)) b = 0u;
-                    da = pow2(-exp_for(pair_most(a)));
-                    db = pow2(-exp_for(pair_most(b)));
+                for (int i = 0; i < 4; i++) {
+                    const bool in = (there >> (i / 2) & 1) && j * kKeys + lane + 32 * i < keys;
+                    pair[i] = in ? reinterpret_cast<const uint32_t *>(blk + (i / 2) * T::kPage + Kv4<D>::kCodes)[lane + 32 * (i & 1)] : 0u;
+                    const float size = pair_most(pair[i]);
+                    least = fminf(least, size != 0.0f ? size : pair_bad(pair[i]) ? 0.0f : INFINITY);
+                    most = fmaxf(most, size);
                 }
-                const float sa = kv4_step(a) * da, sb = kv4_step(b) * db;
-                s0[t] = pack_f16(sa * 16777216.0f, sb * 16777216.0f);
-                s1[t] = pack_f16(sa * 1048576.0f, sb * 1048576.0f);
-                m2[t] = pack_f16(kv4_low(a) * da, kv4_low(b) * db);
-            }
-            if (!warp_wait(&bar->v_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
-            // The slot is free: the products of step j - 2 are complete, and they were issued after its softmax.
-            StepInfo &info = bar->info[slot];
-            if (k == 0) {
-                if (lane == 0) info.value_exp = shared;
-                if (apart) {
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        info.value_of[lane + 32 * i] = (uint8_t)(pair_bad(pair[i]) ? kBad : kOffset + exp_for(pair_most(pair[i])));
-                }
-            }
-            warp_arrive(&bar->info_full[slot]);
-            if (++slot == kInfoSlots) slot = 0;
-            const uint32_t sel_lo = odd ? 0x1054u : 0x5410u, sel_hi = odd ? 0x3276u : 0x7632u;
-            uint8_t *dst = sv + s * T::kOp + k * (D * 128);
-            const uint8_t *src = blk + 8 * grp * Kv4<D>::kRow;
-#pragma unroll 1
-            for (int e = 0; e < D / 32; e++) {
-                const int word = 4 * ((e + (grp >> 1)) & (D / 32 - 1)) + qd;
-                uint32_t lo[4], hi[4];
+                const int shared = shared_exp(least, most);
+                const int ve = (shared & (kApart - 1)) - kOffset;
+                const bool apart = shared & kApart;
+                blk += k * T::kPage;
+                const int in = there >> k & 1 ? keys - j * kKeys - k * SHERRY_KV4_PAGE - 8 * grp : 0;  // tokens of the eight that are there
+                uint32_t s0[4], s1[4], m2[4];
+                const float down = pow2(-ve);
 #pragma unroll
                 for (int t = 0; t < 4; t++) {
-                    const uint32_t a = *reinterpret_cast<const uint32_t *>(src + (2 * t + odd) * Kv4<D>::kRow + 4 * word);
-                    const uint32_t b = *reinterpret_cast<const uint32_t *>(src + (2 * t + 1 - odd) * Kv4<D>::kRow + 4 * word);
-                    lo[t] = prmt(a, b, sel_lo);
-                    hi[t] = prmt(a, b, sel_hi);
+                    const uint2 u = *reinterpret_cast<const uint2 *>(blk + Kv4<D>::kCodes + 4 * (8 * grp + 2 * t));
+                    uint32_t a = 2 * t < in ? u.x : 0u, b = 2 * t + 1 < in ? u.y : 0u;
+                    float da = down, db = down;
+                    if (apart) {
+                        if (pair_bad(a)) a = 0u;
+                        if (pair_bad(b)) b = 0u;
+                        da = pow2(-exp_for(pair_most(a)));
+                        db = pow2(-exp_for(pair_most(b)));
+                    }
+                    const float sa = kv4_step(a) * da, sb = kv4_step(b) * db;
+                    s0[t] = pack_f16(sa * 16777216.0f, sb * 16777216.0f);
+                    s1[t] = pack_f16(sa * 1048576.0f, sb * 1048576.0f);
+                    m2[t] = pack_f16(kv4_low(a) * da, kv4_low(b) * db);
                 }
-                uint8_t *row = dst + 8 * word * 128;
+                if (!warp_wait(&bar->v_empty[s], ((j >> 1) & 1) ^ 1, abort, p.err, limit)) break;
+                // The slot is free: the products of step j - 2 are complete, and they were issued after its softmax.
+                StepInfo &info = bar->info[slot];
+                if (k == 0) {
+                    if (lane == 0) info.value_exp = shared;
+                    if (apart) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    uint32_t y[4];
-#pragma unroll
-                    for (int t = 0; t < 4; t++) y[t] = (i < 4 ? lo[t] : hi[t]) >> (4 * (i & 2));
-                    *reinterpret_cast<uint4 *>(row + i * 128 + ((grp ^ i) << 4)) =
-                        make_uint4(value_pair<0x000F000F>(y[0], s0[0], m2[0]), value_pair<0x000F000F>(y[1], s0[1], m2[1]),
-                                   value_pair<0x000F000F>(y[2], s0[2], m2[2]), value_pair<0x000F000F>(y[3], s0[3], m2[3]));
-                    *reinterpret_cast<uint4 *>(row + (i + 1) * 128 + ((grp ^ (i + 1)) << 4)) =
-                        make_uint4(value_pair<0x00F000F0>(y[0], s1[0], m2[0]), value_pair<0x00F000F0>(y[1], s1[1], m2[1]),
-                                   value_pair<0x00F000F0>(y[2], s1[2], m2[2]), value_pair<0x00F000F0>(y[3], s1[3], m2[3]));
+                        for (int i = 0; i < 4; i++)
+                            info.value_of[lane + 32 * i] = (uint8_t)(pair_bad(pair[i]) ? kBad : kOffset + exp_for(pair_most(pair[i])));
+                    }
                 }
-            }
-            fence_proxy_async_smem();
-            warp_arrive(&bar->v_full[s]);
-            warp_arrive(&bar->raw_empty[s]);
+                warp_arrive(&bar->info_full[slot]);
+                if (++slot == kInfoSlots) slot = 0;
+                const uint32_t sel_lo = odd ? 0x1054u : 0x5410u, sel_hi = odd ? 0x3276u : 0x7632u;
+                uint8_t *dst = sv + s * T::kOp + k * (D * 128);
+                const uint8_t *src = blk + 8 * grp * Kv4<D>::kRow;
+#pragma unroll 1
+                for (int e = 0; e < D / 32; e++) {
+                    const int word = 4 * ((e + (grp >> 1)) & (D / 32 - 1)) + qd;
+                    uint32_t lo[4], hi[4];
+#pragma unroll
+                    for (int t = 0; t < 4; t++) {
+                        const uint32_t a = *reinterpret_cast<const uint32_t *>(src + (2 * t + odd) * Kv4<D>::kRow + 4 * word);
+                        const uint32_t b = *reinterpret_cast<const uint32_t *>(src + (2 * t + 1 - odd) * Kv4<D>::kRow + 4 * word);
+                        lo[t] = prmt(a, b, sel_lo);
+                        hi[t] = prmt(a, b, sel_hi);
+                    }
+                    uint8_t *row = dst + 8 * word * 128;
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int t = 0; t < 4; t++) y[t] = (i < 4 ? lo[t] : hi[t]) >> (4 * (i & 2));
+                        *reinterpret_cast<uint4 *>(row + i * 128 + ((grp ^ i) << 4)) =
+                            make_uint4(value_pair<0x000F000F>(y[0], s0[0], m2[0]), value_pair<0x000F000F>(y[1], s0[1], m2[1]),
+                                       value_pair<0x000F000F>(y[2], s0[2], m2[2]), value_pair<0x000F000F>(y[3], s0[3], m2[3]));
+                        *reinterpret_cast<uint4 *>(row + (i + 1) * 128 + ((grp ^ (i + 1)) << 4)) =
+                            make_uint4(value_pair<0x00F000F0>(y[0], s1[0], m2[0]), value_pair<0x00F000F0>(y[1], s1[1], m2[1]),
+                                       value_pair<0x00F000F0>(y[2], s1[2], m2[2]), value_pair<0x00F000F0>(y[3], s1[3], m2[3]));
+                    }
+                }
+                fence_proxy_async_smem();
+                warp_arrive(&bar->v_full[s]);
+                warp_arrive(&bar->raw_empty[s]);
         }
         }
     } else {
         regs_down<64>();
         if (warp == 13) {
-        // ---------------- pages ----------------
-        if (lane == 0) {
-            int it = 0;
-            for (; it < steps; it++) {
-                const int s = it & 1;
-                int page[2], there = 0;
+            // ---------------- pages ----------------
+            if (lane == 0) {
+                int it = 0;
+                for (; it < steps; it++) {
+                    const int s = it & 1;
+                    int page[2], there = 0;
 #pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const int t0 = it * kKeys + k * SHERRY_KV4_PAGE;
-                    page[k] = t0 < keys ? __ldg(p.c.table + (long long)w.b * p.c.table_stride + t0 / SHERRY_KV4_PAGE) : -1;
-                    if (page[k] >= 0 && page[k] < p.c.pages) there |= 1 << k;
-                    else if (t0 < keys) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
-                }
-                if (!mbar_wait(&bar->raw_empty[s], ((it >> 1) & 1) ^ 1, abort, p.err, limit)) break;
-                bar->there[s] = there;
-                if (there == 0) {
-                    mbar_arrive(&bar->raw_full[s]);
-                    continue;
-                }
-                mbar_arrive_expect_tx(&bar->raw_full[s], (there == 3 ? 2 : 1) * T::kPage);
+                    for (int k = 0; k < 2; k++) {
+                        const int t0 = it * kKeys + k * SHERRY_KV4_PAGE;
+                        page[k] = t0 < keys ? __ldg(p.c.table + (long long)w.b * p.c.table_stride + t0 / SHERRY_KV4_PAGE) : -1;
+                        if (page[k] >= 0 && page[k] < p.c.pages) there |= 1 << k;
+                        else if (t0 < keys) atomicCAS(p.err, 0u, (unsigned int)SHERRY_ERR_INDEX);
+                    }
+                    if (!mbar_wait(&bar->raw_empty[s], ((it >> 1) & 1) ^ 1, abort, p.err, limit)) break;
+                    bar->there[s] = there;
+                    if (there == 0) {
+                        mbar_arrive(&bar->raw_full[s]);
+                        continue;
+                    }
+                    mbar_arrive_expect_tx(&bar->raw_full[s], (there == 3 ? 2 : 1) * T::kPage);
 #pragma unroll
-                for (int k = 0; k < 2; k++)
-                    if (there >> k & 1)
-                        bulk_load(smem_u32(raw + (2 * s + k) * T::kPage), kv4_block<D>(p.c, page[k], h, 0), T::kPage, &bar->raw_full[s]);
+                    for (int k = 0; k < 2; k++)
+                        if (there >> k & 1)
+                            bulk_load(smem_u32(raw + (2 * s + k) * T::kPage), kv4_block<D>(p.c, page[k], h, 0), T::kPage, &bar->raw_full[s]);
+                }
+                // every copy lands before shared memory is released
+                volatile int no_abort = 0;
+                for (int j = it < 2 ? 0 : it - 2; j < it; j++) mbar_wait(&bar->raw_full[j & 1], (j >> 1) & 1, &no_abort, p.err, kDrainLimit);
             }
-            // every copy lands before shared memory is released
-            volatile int no_abort = 0;
-            for (int j = it < 2 ? 0 : it - 2; j < it; j++) mbar_wait(&bar->raw_full[j & 1], (j >> 1) & 1, &no_abort, p.err, kDrainLimit);
-        }
         } else if (warp == 12 && steps > 0) {
             // ---------------- products ----------------
             // The whole warp walks and waits, one elected lane issues.
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) attn_tile_kernel(const __grid
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-mma_ts_all<0, kKeys / 16, D>(tmem + 2 * kKeys + i * D, tmem + i * kKeys, v_lo + s * (T::kOp >> 4),
+                        mma_ts_all<0, kKeys / 16, D>(tmem + 2 * kKeys + i * D, tmem + i * kKeys, v_lo + s * (T::kOp >> 4),
                                                      kIdesc<D>, j != 0);
                         if (j + 1 == steps) umma_commit(&bar->o_full[i]);
                     }

@@ -39,7 +39,8 @@ attention few rows: x_t = scale * q.k_t is summed in fp32 on codes 0 .. 15: D / 
           each, or 2^-25 of units in which the largest of the token is at least 2^-14: 2^-10 of |k| or |v| in
           all; probabilities 2^-11: |dx_t| += |scale| sum|q| |k_t| 2^-10, dv_t = |v_t| (2^-10 + 2^-11).
           Products p s (p v) that are below fp16's normal range are off by 2^-25 where the row's largest is at
-          least 2^6 (2^-4, in the tiles' units): at most 2^-26 of the largest for each token.
+          least 2^5: 2^-30 of it for each token, times |c - 8| <= 8.  In the tiles P is off by 2^-25 where the
+          largest is at least 2^9, and values are at most 2^-6, the largest's own at least 2^-14: 2^-26 of it.
 """
 import ctypes
 
@@ -860,6 +861,7 @@ def test_constant_value_rows(value, ctx, new, same, D, wide):
     out = call(bt.dev(), q, max_q=max(new))
     assert S.device_error() == 0
     check_rows(bt, q, out, 8, D ** -0.5, heads=[0, 5])
+    # the low end and the result are each rounded to bf16, half a step of 2^-8
     assert torch.all((out.double() / (value or 1.0) - (1.0 if value else 0.0)).abs() <= 2.0 ** -7)
 
 
@@ -1001,6 +1003,7 @@ def test_tiles_constant_value_rows(value, D):
     q = bf16_randn(bt.rng, (bt.T, 32, D))
     out = call(bt.dev(), q)
     assert S.device_error() == 0
+    # the low end and the result are each rounded to bf16, half a step of 2^-8
     assert torch.all((out.double() / (value or 1.0) - (1.0 if value else 0.0)).abs() <= 2.0 ** -7)
 
 

@@ -25,11 +25,12 @@ namespace {
 // Decoding is what bounds it next (integer instructions, half of an SM's rate): a code's four bits at the
 // bottom of a half word are the fp16 c 2^-24, one up c 2^-20, so a word of eight codes takes a shift and
 // four ANDs; the keys' powers of two go into q (fp16, exact after a power of two per row).
-// 32 sequences of 32,768 tokens, 8 heads of 128, 4 query heads each (floor 177 us): 219 us, 5.2 TB/s, 1,090
-// instructions a page, two thirds of them integer.  Earlier forms: a page shared by four warps and filled
-// by a fifth, 357 us; a warp per page with codes as bf16 128 + c (a shift and an OR more per pair), 320 us;
-// selects for unseen tokens on every page and 64-bit divisions in the walk, 234 us.  Short contexts are
-// latency: two pages 5.8 us as a cluster, 8.8 as runs and a join.
+// 32 sequences of 32,768 tokens, 8 heads of 128, 4 query heads each (floor 177 us): 209 us in a graph, 5.5
+// TB/s, 935 instructions a page; 232 us in calls back to back.  Earlier forms: a page shared by four warps and
+// filled by a fifth, 357 us; a warp per page with codes as bf16 128 + c (a shift and an OR more per pair),
+// 320 us; selects for unseen tokens on every page and 64-bit divisions in the walk, 234 us; the softmax on
+// single floats, 1,090 instructions, 220 us; the first page's references set before its first pass, 217 us.
+// Short contexts are latency: two pages 6.1 us as a cluster, 8.9 as runs and a join.
 constexpr int kFewWarps = 4;
 constexpr int kFewThreads = 32 * kFewWarps;
 constexpr int kFewRunsMax = 2560;  // bounds the workspace
@@ -840,9 +841,9 @@ sherry_status few_launch(AttnParams p, cudaStream_t stream) {
     // A cluster per row tile, or equal runs and a join.  In pages one after the other, if every sequence is as
     // long as its table: the largest cluster of which all are resident at once, against the runs and about
     // kJoinPages for the join and its launch.  Clusters and runs, us, one new token and 8 heads each: one
-    // sequence of 2,048 tokens, heads of 64, 6.4 and 10.9; of 8,192, 10.3 and 14.5; 16 of 2,048, heads of 128,
-    // 19.2 and 22.6 (clusters of 2; of 8, in more than one wave, 30.7); 64 of 1,024, heads of 64, in waves
-    // 59.5 and 26.0.
+    // sequence of 2,048 tokens, heads of 64, 6.6 and 10.9; of 8,192, 10.5 and 14.5; 16 of 2,048, heads of 128,
+    // 18.7 and 22.8 (clusters of 2; of 8, in more than one wave, 31.0); 64 of 1,024, heads of 64, clusters of 8
+    // in waves 61.9 and 24.7 (of 2, in waves too, 21.0: the rule passes those by).
     const long long slots = (long long)sm_count() * bps, width = p.c.width;
     const long long by_runs = (even * width + slots * kFewWarps - 1) / (slots * kFewWarps) + kJoinPages;
     auto clusters = [&](auto size) {
@@ -880,8 +881,8 @@ namespace {
 // kernel spreads a sequence's pages over the machine but decodes them again for every 16 rows; the tile
 // kernel decodes once for 256 rows, one CTA to a key/value head however long the context.  Measured, per
 // page of context: 0.25 to 0.35 us for 16 rows of a head on one SM, against 1.0 to 1.2 us for 256 (heads
-// of 64 and 128).  E.g. 8 heads, 8,192 tokens, heads of 64: 256 rows 40 us against 133, 1,024 rows 124
-// against 133, 2,048 rows 235 against 134; 32 sequences of 4,096, 32 rows each: 76 against 142.
+// of 64 and 128).  E.g. 8 heads, 8,192 tokens, heads of 64: 256 rows 39 us against 135, 1,024 rows 122
+// against 136, 2,048 rows 230 against 136.
 bool few_is_faster(const sherry_kv4 *c, int g) {
     const long long rows = c->T * g, sms = sm_count();
     const long long few = c->H * (rows / 16 + c->B), tile = c->H * (rows / 256 + c->B);

@@ -28,7 +28,8 @@
 // by the products, whose scores alone take all of its bandwidth while they run).  Measured: 3,900; 4,500.
 // A tile's softmax (about 2,300 clocks with two of them on the exponentials' unit) and its products (600;
 // 1,300) follow each other, and the other tile fills only part of the gap.  4 prompts' chunks of 4,096 tokens
-// at 16,384, 32 heads of 128 over 8: 3.9 ms, 960 TFLOP/s; a prompt of 2,048, heads of 64: 47 us.
+// at 16,384, 32 heads of 128 over 8: 3.8 ms in a graph, 1,010 TFLOP/s (4.0 ms in calls with changing inputs); a
+// prompt of 2,048, heads of 64: 47.6 us.
 // Tried, in clocks per step with heads of 128 unless said otherwise:
 //   codes as operands, steps and low ends applied by the softmax threads from shared memory: 8,000
 //   the present operands, code unrolled over the step (four roles' straight-line code does not fit the

@@ -187,6 +187,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 //     p = 2^(x - ref),   l = sum p,   corr = sum p (m + 8 s),   o = sum fp16(p s 2^-ve) c.
 // ref is a whole number, kDown above the largest score when it was set; it moves when p passes 2^-8, so that
 // the weights of 65,536 equal tokens sum to no more than 2^8 and l and corr stay in fp32's range for any value.
+// (Weights below 2^-110 of the row's largest are flushed: the price of kDown, of which 2^-126 leaves 2^-110.)
 // ve follows the largest p s that the row met, not the largest s: tokens that the row does not see, or that have
 // no weight in it, cost the others nothing (one power for all rows and tokens, and one reference for l and o,
 // gave inf for a constant value row of 2^22 and zeros beside an unseen value of 1e30).  The largest p s 2^-ve is

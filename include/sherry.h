@@ -562,13 +562,14 @@ sherry_status sherry_kv4_read(const sherry_kv4 *c, void *k, void *v, int type, i
  * head h, with the cache's head h / (Hq / H):
  *     out = sum_t p[t] v[t],  p = softmax over t = 0 .. pos of scale * (q . k[t]),
  * with k and v the values the cache holds.  A row without a position (pos < 0) gives zeros.
- * Sums and softmax statistics are fp32, the result is rounded once to bf16 (queries beyond
- * 2^112, scores beyond 2^30 and sums of values beyond fp32 are not served).  Few new tokens: the first product runs on the codes, exactly,
- * and a probability times its token's step is rounded to fp16 for the second: 2^-11 relative, down to
- * 2^-21 of the row's largest such product, 2^-32 of that below.  Many (prompts): keys, values and
- * probabilities are rounded to fp16 after powers of two that bring them into its range, 2^-10
- * relative to the largest element of a token's row in all; the powers of values belong to the tokens
- * and to the rows that see them, so a row's accuracy is that of what it sees and gives weight.
+ * Sums and softmax statistics are fp32, the result is rounded once to bf16.  Queries beyond 2^112,
+ * scores beyond 2^30 and sums of values beyond fp32 are not served.
+ * Few new tokens: the first product runs on the codes, exactly, and a probability times its token's
+ * step is rounded to fp16 for the second: 2^-11 relative, down to 2^-21 of the row's largest such
+ * product, 2^-32 of that below; weights below 2^-110 of the row's largest count as none.
+ * Many (prompts): keys, values and probabilities are rounded to fp16 after powers of two that bring
+ * them into its range, 2^-10 relative to the largest element of a token's row in all.
+ * In both a row's accuracy is that of the tokens it sees and gives weight, whatever the others hold.
  * A key or value of NaN makes the rows that see it NaN, and no others.
  *   q    [T][Hq][D] bf16, 16-byte aligned, q_stride as above; Hq a multiple of H.
  *   out  [T][Hq][D] bf16, likewise.

@@ -582,7 +582,8 @@ def device_error():
 
 def set_wait_limit(cycles):
     """Limit (SM clock cycles) of the kernels' bounded barrier waits, for
-    kernels launched afterwards by this process; 0 restores the default."""
+    kernels launched afterwards by this process; 0 restores the default, and with 1
+    the attention's waits for pages of few new tokens give up without a look."""
     _check(lib().sherry_set_wait_limit(int(cycles)), "sherry_set_wait_limit")
 
 
